@@ -8,6 +8,10 @@ library raises.
     bm = create_block_mask("and", [("causal",)], B=1, H=1, q_len=S, kv_len=S)
     o, lse = flex_attention(q, k, v, bm, score_mod=("alibi", slopes))
 
+Around a paged cache: paged_append (new keys and values, rotary positions on the way),
+flex_decode_paged (a few query tokens per sequence, each sequence with its own length),
+flex_decode_shared (a batch that shares a long prefix), and rope_apply / rope_autograd.
+
 Mask leaves: ("causal",), ("sliding", W), ("document",), ("prefix", P), combined
 by "and" / "or" ("Concepts": mask_mod, Composing masks).  Score mods: None,
 ("alibi", slopes[Hq] fp32), ("softcap", cap), ("bias", bias[B, Hq, Sq, Skv] bf16),
@@ -19,10 +23,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflexattn.so")
@@ -32,13 +38,16 @@ BLOCK_SIZE = 128
 MAX_LEAVES = 4
 LEAF = {"causal": 0, "sliding": 1, "document": 2, "prefix": 3}
 OP = {"and": 0, "or": 1}
+ROPE_SCALING = {"linear": 1, "base": 2, "bands": 3, "yarn": 4}
 SCORE = {"none": 0, "alibi": 1, "softcap": 2, "bias": 3, "bias_softcap": 4}
 
 EXPORTS = ("fa_status_string", "fa_block_mask_shape", "fa_create_block_mask", "fa_create_block_mask_unsplit",
            "fa_workspace_size", "fa_backward_workspace_size", "fa_backward", "fa_forward_paged",
            "fa_decode_workspace_size", "fa_decode",
            "fa_forward", "fa_get_device_status", "fa_set_watchdog_ms", "fa_set_selftest_stall",
-           "fa_forward_static_scratch")
+           "fa_forward_static_scratch", "fa_rope_frequencies", "fa_rope_apply", "fa_paged_append",
+           "fa_decode_paged_workspace_size", "fa_decode_paged", "fa_decode_shared_workspace_size",
+           "fa_decode_shared")
 
 
 class FlexAttnError(RuntimeError):
@@ -71,6 +80,16 @@ class TensorDesc(ctypes.Structure):
 class ScoreModDesc(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p), ("bias_strides", ctypes.c_int64 * 4)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
+
+
+class RopeScalingDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("rot_lo", ctypes.c_double), ("rot_hi", ctypes.c_double)]
 
 
 def _load():
@@ -107,6 +126,18 @@ def _load():
     lib.fa_forward_static_scratch.argtypes = [ctypes.POINTER(TensorDesc)] * 3 + [
         ctypes.POINTER(BlockMaskDesc), ctypes.POINTER(ScoreModDesc), ctypes.c_float,
         ctypes.POINTER(TensorDesc), vp, vp]
+    td, ci, sz, f32 = ctypes.POINTER(TensorDesc), ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    rope, score = ctypes.POINTER(RopeDesc), ctypes.POINTER(ScoreModDesc)
+    lib.fa_rope_frequencies.argtypes = [ci, ctypes.c_double, ctypes.POINTER(RopeScalingDesc),
+                                        ctypes.POINTER(ctypes.c_double), ctypes.POINTER(f32)]
+    lib.fa_rope_apply.argtypes = [td, td, rope, vp, i64, i64, ci, td, td, vp]
+    lib.fa_paged_append.argtypes = [td, td, td, rope, vp, vp, vp, i64, i64, td, td, td, vp, sz, vp]
+    lib.fa_decode_paged_workspace_size.argtypes = [i64] * 5
+    lib.fa_decode_paged_workspace_size.restype = sz
+    lib.fa_decode_paged.argtypes = [td, td, td, vp, i64, i64, vp, i64, score, f32, td, vp, vp, sz, vp]
+    lib.fa_decode_shared_workspace_size.argtypes = [i64] * 6
+    lib.fa_decode_shared_workspace_size.restype = sz
+    lib.fa_decode_shared.argtypes = lib.fa_decode_paged.argtypes
     return lib
 
 
@@ -466,6 +497,265 @@ class FlexAttentionFunction(torch.autograd.Function):
 def flex_attention_autograd(q, k, v, block_mask: BlockMask, score_mod=None, scale: Optional[float] = None):
     """Differentiable flex_attention: returns (out, lse); out.backward() runs fa_backward."""
     return FlexAttentionFunction.apply(q, k, v, block_mask, score_mod, scale)
+
+
+# ------------------------------------------------------------------ rotary positions, paged cache
+
+_I64x4 = ctypes.c_int64 * 4
+
+
+def _placed(fn):
+    """Run fn on the device of its first argument and, when given, on `stream` (fn's own
+    tensors are then allocated for that stream)."""
+    @functools.wraps(fn)
+    def call(x, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        if not (isinstance(x, torch.Tensor) and x.is_cuda):
+            raise TypeError(f"{fn.__name__}: expected CUDA tensors")
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
+            with torch.cuda.stream(stream):
+                return fn(x, *args, **kw)
+        if x.device.index != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return fn(x, *args, **kw)
+        return fn(x, *args, **kw)
+    return call
+
+
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """t itself, or a contiguous copy where its strides or alignment are not ones the
+    kernels read (16-byte vectors along D, no expanded dimension)."""
+    if t.dim() == 4 and t.numel():
+        st = t.stride()
+        if st[3] != 1 or (st[0] | st[1] | st[2]) & 7 or t.data_ptr() & 15 or (0 in st and _expanded(t)):
+            return t.contiguous() if not t.is_contiguous() else t.clone()
+    return t
+
+
+def _desc(t: torch.Tensor, device: torch.device, what: str) -> TensorDesc:
+    if t.dtype != torch.bfloat16 or t.dim() != 4 or t.device != device:
+        raise TypeError(f"{what}: expected a 4-D bf16 tensor on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return TensorDesc(t.data_ptr(), _I64x4(*t.shape), _I64x4(*t.stride()))
+
+
+def _ints(t: torch.Tensor, shape: tuple, device: torch.device, what: str) -> int:
+    """Address of an int32 tensor of the given shape (None: any size), its last dimension contiguous."""
+    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)) or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise TypeError(f"{what}: expected int32 {list(shape)} on {device} with a contiguous last dimension, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, amplitude: float, device: torch.device) -> RopeDesc:
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
+            (inv_freq.shape[0] > 1 and inv_freq.stride(0) != 1):
+        raise TypeError(f"inv_freq: expected a contiguous fp64 tensor [rotary_dim / 2] on {device}")
+    if not amplitude > 0:
+        raise ValueError("amplitude must be positive")
+    return RopeDesc(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude)
+
+
+_paged_workspaces = {}
+_STATUS_BYTES = int(_lib.fa_workspace_size())
+
+
+def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
+    """The workspace paged_append, flex_decode_paged and flex_decode_shared use by
+    default: one per device and stream, zero-filled when allocated; a larger one takes
+    over its predecessor's status word (the predecessor is kept alive).  While a CUDA
+    graph is captured each call gets a zero-filled workspace of the graph's own instead
+    (pass ws= to read the status of captured calls)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros((max(need, _STATUS_BYTES),), dtype=torch.uint8, device=device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    kept = _paged_workspaces.setdefault((index, torch.cuda.current_stream(index).cuda_stream), [])
+    if not kept or kept[-1].numel() < need:
+        ws = torch.zeros((max(need, 1 << 22),), dtype=torch.uint8, device=device)
+        if kept:
+            ws[:_STATUS_BYTES].copy_(kept[-1][:_STATUS_BYTES])
+        kept.append(ws)
+    return kept[-1]
+
+
+def _given_workspace(ws: torch.Tensor, need: int, device: torch.device, what: str) -> torch.Tensor:
+    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise TypeError(f"{what}: ws must be a contiguous uint8 tensor on {device}")
+    if ws.numel() < need:
+        raise FlexAttnError(FA_ERR_INVALID_ARG, f"{what}: workspace of {ws.numel()} bytes, {need} needed")
+    return ws
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[tuple] = None,
+                     device=None) -> Tuple[torch.Tensor, float]:
+    """Frequencies of rotary positions (fa_rope_frequencies): (inv_freq fp64
+    [rotary_dim / 2] on the device, amplitude).  scaling: None, ("linear", factor),
+    ("base", factor), ("bands", factor, original_len, rot_lo, rot_hi) or ("yarn", factor,
+    original_len, rot_lo, rot_hi) with rot_lo < rot_hi in turns over original_len."""
+    sc = None
+    if scaling is not None:
+        if scaling[0] not in ROPE_SCALING:
+            raise ValueError(f"unknown rope scaling {scaling[0]!r}")
+        if len(scaling) != (2 if scaling[0] in ("linear", "base") else 5):
+            raise ValueError(f"rope scaling {scaling[0]!r}: wrong number of parameters")
+        sc = RopeScalingDesc(ROPE_SCALING[scaling[0]], *[float(x) for x in scaling[1:]])
+    host = (ctypes.c_double * max(1, rotary_dim // 2))()
+    amplitude = ctypes.c_float()
+    _check(_lib.fa_rope_frequencies(rotary_dim, base, ctypes.byref(sc) if sc is not None else None, host,
+                                    ctypes.byref(amplitude)), "fa_rope_frequencies")
+    inv_freq = torch.tensor(list(host), dtype=torch.float64)
+    return inv_freq.to(device if device is not None else "cuda"), amplitude.value
+
+
+@_placed
+def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
+               positions: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
+               inverse: bool = False, offset: int = 0, out: Optional[tuple] = None):
+    """Rotary positions on q [B,Hq,S,D] and k [B,Hk,S,D] (or None) through fa_rope_apply:
+    returns (q_out, k_out).  inv_freq: fp64 [rotary_dim / 2] (rope_frequencies), the
+    first rotary_dim elements of a head are turned.  positions: int32 [B,S] or [S] (None:
+    offset + s).  inverse=True turns the other way, which takes the gradients of the
+    outputs to those of q and k.  out: (q_out, k_out), which may be (q, k).  stream=:
+    the CUDA stream to run on."""
+    device = q.device
+    rope = _rope_desc(inv_freq, interleaved, amplitude, device)
+    q = _readable(q)
+    k = _readable(k) if k is not None else None
+    if out is None:
+        out = (torch.empty_like(q), torch.empty_like(k) if k is not None else None)
+    q_out, k_out = out
+    if (k is None) != (k_out is None):
+        raise ValueError("rope_apply: out holds an output for each of q and k")
+    qd, qo = _desc(q, device, "q"), _desc(q_out, device, "out[0]")
+    kd, ko = (_desc(k, device, "k"), _desc(k_out, device, "out[1]")) if k is not None else (None, None)
+    pos, pos_stride = None, 0
+    if positions is not None:
+        B, S = q.shape[0], q.shape[2]
+        pos = _ints(positions, (S,) if positions.dim() == 1 else (B, S), device, "positions")
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    _check(_lib.fa_rope_apply(qd, kd, rope, pos, pos_stride, offset, 1 if inverse else 0, qo, ko,
+                              torch.cuda.current_stream().cuda_stream), "fa_rope_apply")
+    return out
+
+
+class RopeFunction(torch.autograd.Function):
+    """rope_apply as a torch autograd function (no gradient for the frequencies)."""
+
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, interleaved, amplitude, offset):
+        ctx.save_for_backward(inv_freq, positions)
+        ctx.opts = dict(interleaved=interleaved, amplitude=amplitude, offset=offset)
+        out = rope_apply(q, k, inv_freq, positions=positions, **ctx.opts)
+        return out if k is not None else out[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_q, grad_k=None):
+        inv_freq, positions = ctx.saved_tensors
+        gq, gk = rope_apply(grad_q, grad_k, inv_freq, positions=positions, inverse=True, **ctx.opts)
+        return gq, gk, None, None, None, None, None
+
+
+def rope_autograd(q, k, inv_freq, positions=None, interleaved: bool = False, amplitude: float = 1.0, offset: int = 0):
+    """Differentiable rope_apply: returns (q_out, k_out)."""
+    out = RopeFunction.apply(q, k, inv_freq, positions, interleaved, amplitude, offset)
+    return out if k is not None else (out, None)
+
+
+@_placed
+def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 page_table: torch.Tensor, cache_lens: torch.Tensor, new_lens: Optional[torch.Tensor] = None,
+                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
+                 ws: Optional[torch.Tensor] = None):
+    """Append k, v [B,Hkv,S,D] to a paged cache (fa_paged_append): token s of sequence b
+    goes to position cache_lens[b] + s, rotated there when inv_freq is given (k, and q
+    [B,Hq,S,D] into q_out), if s < new_lens[b] (None: all).  k_pages / v_pages
+    [num_pages,Hkv,128,D] are written in place; page_table int32 [B, pages],
+    cache_lens / new_lens int32 [B] are not changed.  Returns q_out (None without q;
+    rows past new_lens are left as they were, zero in a q_out made here).  Bad lengths
+    and pages: device_status(ws)."""
+    device = k.device
+    k, v = _readable(k), _readable(v)
+    B = k.shape[0]
+    kd, vd = _desc(k, device, "k"), _desc(v, device, "v")
+    kp, vp = _desc(k_pages, device, "k_pages"), _desc(v_pages, device, "v_pages")
+    table = _ints(page_table, (B, None), device, "page_table")
+    have = _ints(cache_lens, (B,), device, "cache_lens")
+    fresh = _ints(new_lens, (B,), device, "new_lens") if new_lens is not None else None
+    rope = _rope_desc(inv_freq, interleaved, amplitude, device) if inv_freq is not None else None
+    qd = qo = None
+    if q is not None:
+        q = _readable(q)
+        if q_out is None:
+            q_out = torch.empty_like(q) if new_lens is None else torch.zeros_like(q)
+        qd, qo = _desc(q, device, "q"), _desc(q_out, device, "q_out")
+    elif q_out is not None:
+        raise ValueError("paged_append: q_out without q")
+    ws = paged_workspace(device) if ws is None else _given_workspace(ws, _STATUS_BYTES, device, "fa_paged_append")
+    _check(_lib.fa_paged_append(kd, vd, qd, rope, have, fresh, table, page_table.stride(0), page_table.shape[1], kp, vp,
+                                qo, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream),
+           "fa_paged_append")
+    return q_out
+
+
+def _decode_pages(name, fn, need, q, k_pages, v_pages, page_table, seq_lens, extra, score_mod, scale, out, lse, ws):
+    device = q.device
+    q = _readable(q)
+    B, Hq, n, D = q.shape
+    if out is None:
+        out = torch.empty((B, Hq, n, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((B, Hq, n), dtype=torch.float32, device=device)
+    elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (B, Hq, n) or not lse.is_contiguous():
+        raise TypeError(f"lse: expected a contiguous fp32 tensor [B, Hq, q_len] on {device}")
+    qd, od = _desc(q, device, "q"), _desc(out, device, "out")
+    kp, vp = _desc(k_pages, device, "k_pages"), _desc(v_pages, device, "v_pages")
+    table = _ints(page_table, (B, None), device, "page_table")
+    lens = _ints(seq_lens, (B,), device, "seq_lens")
+    sm = None
+    if score_mod is not None:
+        sm, _ = score_mod_desc(score_mod)
+        if score_mod[0] == "alibi" and (score_mod[1].shape != (Hq,) or score_mod[1].device != device):
+            raise TypeError(f"ALiBi slopes: fp32 [Hq] on {device}")
+    ws = paged_workspace(device, need) if ws is None else _given_workspace(ws, need, device, name)
+    _check(fn(qd, kp, vp, table, page_table.stride(0), page_table.shape[1], lens, extra, sm,
+              scale if scale is not None else 0.0, od, lse.data_ptr(), ws.data_ptr(), ws.numel(),
+              torch.cuda.current_stream().cuda_stream), name)
+    return out, lse
+
+
+@_placed
+def flex_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      seq_lens: torch.Tensor, window: Optional[int] = None, score_mod=None,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """FlexDecoding over a paged cache (fa_decode_paged): q [B,Hq,q_len,D], at most 16
+    query rows per kv head ((Hq / Hkv) * q_len), k_pages / v_pages [num_pages,Hkv,128,D],
+    page_table int32 [B, pages], seq_lens int32 [B] (each sequence's keys, the new tokens'
+    included).  Query token i of sequence b sits at position seq_lens[b] - q_len + i and
+    attends the keys at or before it, with window= also at or after it - window.
+    score_mod: None, ("alibi", slopes) or ("softcap", cap).  Returns (out, lse)."""
+    if window is not None and window < 0:
+        raise ValueError("flex_decode_paged: window must not be negative")
+    need = int(_lib.fa_decode_paged_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3]))
+    return _decode_pages("fa_decode_paged", _lib.fa_decode_paged, need, q, k_pages, v_pages, page_table, seq_lens,
+                         -1 if window is None else window, score_mod, scale, out, lse, ws)
+
+
+@_placed
+def flex_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                       seq_lens: torch.Tensor, prefix_len: int, score_mod=None, scale: Optional[float] = None,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None):
+    """flex_decode_paged for sequences that share their first prefix_len keys (a multiple
+    of 128: the first prefix_len / 128 entries of every row of page_table are the same
+    pages), which are taken once for the whole batch (fa_decode_shared)."""
+    need = int(_lib.fa_decode_shared_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3],
+                                                    prefix_len))
+    return _decode_pages("fa_decode_shared", _lib.fa_decode_shared, need, q, k_pages, v_pages, page_table, seq_lens,
+                         prefix_len, score_mod, scale, out, lse, ws)
 
 
 def device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:

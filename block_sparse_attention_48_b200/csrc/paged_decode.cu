@@ -1,0 +1,586 @@
+// Decoding against a paged cache for sm_100a: a few query tokens per sequence,
+// every sequence with its own length ("Flex Attention" paper review sec. 3.1, the
+// decoding template, and sec. 4.5, paged attention; rocketrecap talk: the work is
+// split along the KV dimension and the partial results are reduced at the end).
+//
+//   row (h, i) of sequence b sits at position len_b - q_len + i and attends the keys
+//   at or before it (and within the window);  out = softmax(mod(q k^T scale)) v
+//
+// Bound: HBM (K and V of the pages are read once; 4 G flops per byte of them).
+// Work split: the pages of all (sequence, kv head) segments form one list, and CTA c
+// of a grid of one CTA per SM takes its c-th equal share, so every SM streams the
+// same number of bytes whatever the lengths are.  Each CTA finds its share by a scan
+// of the lengths.  K and V arrive by TMA in a ring; each of the eight compute warps
+// takes 16 keys of every page, the group's query rows being the n = 8 side of
+// m16n8k16 MMAs, with an online softmax of its own.  At the end of a piece of a
+// segment the warps' states are joined in shared memory.  A piece that is a whole
+// segment is written out at once; else its state goes to the workspace and the CTA
+// that completes the segment (a counter, which wraps back to zero) joins
+// the pieces in list order, so that results do not depend on who comes last.
+//
+// Places outside a row's keys may hold anything (a page's slots behind the last key
+// are not initialised, and masked keys may hold infinities or NaN): their scores are
+// replaced, not added to, and values that no row attends are zeroed before the product.
+#include <mutex>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "context.cuh"
+#include "flex_fwd.cuh"
+#include "flexattn.h"
+#include "paged_decode.cuh"
+#include "paged_walk.cuh"
+#include "ptx.cuh"
+#include "score_math.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kBox = 16384;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, int NR>
+struct PdCfg {
+    static constexpr int TILE = 128 * D * 2;       // K or V of one page and kv head
+    static constexpr int NS = D == 128 ? 2 : 4;    // ring stages, 128 KB in flight per SM
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int OROW = D + 4;             // padded row of the joining buffer (bank spread)
+    static constexpr int OFF_JOIN = NS * STAGE;
+    static constexpr int SMEM = OFF_JOIN + kPdWarps * 8 * NR * OROW * 4 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory beyond 227 KB per CTA");
+};
+
+struct __align__(16) PdShared {
+    uint64_t full[4], empty[4];
+    long long scan[kPdThreads / 32];
+    long long total;                        // list length
+    int used;                               // CTAs that have work
+    PdWalk start;                           // where this CTA's share starts
+    int last;                               // this CTA completed the segment
+    float m[kPdWarps][kPdMaxRows], l[kPdWarps][kPdMaxRows];
+};
+
+__device__ __forceinline__ void compute_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kPdWarps) : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Address of 16-byte unit `unit` of key row `key` in a tile loaded with the
+// 128-byte swizzle (64-column chunks of 16 KB).
+__device__ __forceinline__ uint32_t swz(uint32_t base, int key, int unit)
+{
+    return base + (uint32_t)((unit >> 3) * kBox + key * 128 + (((unit & 7) ^ (key & 7)) << 4));
+}
+
+// An infinity or NaN among the two bf16 of a register.
+__device__ __forceinline__ bool nonfinite2(uint32_t w)
+{
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// All threads: the list's length and where this CTA's share starts.
+__device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool& bad)
+{
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int per = (p.B + kPdThreads - 1) / kPdThreads;
+    const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
+    long long mine = 0;
+    for (int b = lo; b < hi; ++b) mine += pd_range(p, __ldg(p.seq_lens + b), bad).n;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sh.scan[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kPdThreads / 32; ++w) {
+        before += w < warp ? sh.scan[w] : 0;
+        total += sh.scan[w];
+    }
+    const long long T = total * p.Hkv;
+    const int used = (int)min(T, (long long)p.grid);
+    if (tid == 0) {
+        sh.total = T;
+        sh.used = used;
+    }
+    if ((int)blockIdx.x < used) {
+        const long long x0 = pd_share(T, blockIdx.x, used);
+        long long acc = before + inc - mine;  // pages of the sequences before this thread's
+        if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + mine))
+            pd_find(p, x0, lo, hi, acc, sh.start, bad);
+    }
+    __syncthreads();
+}
+
+template <int D, int SCORE, int NR>
+__global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __grid_constant__ PdParams p)
+{
+    using C = PdCfg<D, NR>;
+    constexpr int KD = D / 16;
+    constexpr int RMAX = 8 * NR;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PdShared sh;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    bool bad = false;
+    Watchdog wd{p.watchdog_ns, false};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kPdWarps);
+        }
+        mbar_fence_init();
+    }
+    pd_locate(p, sh, bad);  // ends with a CTA barrier
+    const long long T = sh.total;
+    const int used = sh.used;
+    const bool works = (int)blockIdx.x < used;
+    const long long x0 = works ? pd_share(T, blockIdx.x, used) : 0;
+    const long long count = works ? pd_share(T, blockIdx.x + 1, used) - x0 : 0;
+    PdWalk w{0, 0, 0, {0, 0, 0, 0}};
+    if (works) w = sh.start;
+
+    if (warp == kPdWarps) {
+        // TMA producer: K and V of every page of the share.  Lane i holds the page of
+        // the (t & ~31) + i-th page of the segment's range.
+        uint32_t issued = 0;
+        bool ok = true;
+        int page_lane = 0, chunk = -1;
+        for (long long i = 0; i < count; ++i, ++issued) {
+            if (chunk != (w.t & ~31)) {
+                chunk = w.t & ~31;
+                const int tt = chunk + lane;
+                page_lane = tt < w.r.n ? __ldg(p.page_table + (int64_t)w.b * p.pt_stride + w.r.lo + tt) : 0;
+            }
+            const int page = pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, w.t & 31), p.num_pages, bad);
+            const uint32_t slot = issued % C::NS, use = issued / C::NS;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.empty[slot], (use & 1) ^ 1, wd));
+            if (!ok) break;
+            if (elect_one_sync()) {
+                uint8_t* dst = smem + slot * C::STAGE;
+                mbar_arrive_expect_tx(&sh.full[slot], C::STAGE);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    tma_load_4d(dst + c * kBox, &p.tm_k, &sh.full[slot], c * 64, 0, w.hk, page);
+                    tma_load_4d(dst + C::TILE + c * kBox, &p.tm_v, &sh.full[slot], c * 64, 0, w.hk, page);
+                }
+            }
+            __syncwarp();
+            if (i + 1 < count) {
+                const int b = w.b;
+                pd_advance(p, w, bad);
+                if (w.b != b) chunk = -1;
+            }
+        }
+        // copies in flight land before the CTA exits (bounded)
+        Watchdog dw{wd.failed ? 1000000ull : wd.limit_ns, false};
+        for (uint32_t j = 0; j < (uint32_t)C::NS && j < issued; ++j) {
+            const uint32_t last = issued - 1 - j;
+            dw.failed = false;
+            mbar_wait(&sh.full[last % C::NS], (last / C::NS) & 1, dw);
+        }
+        if (lane == 0 && (wd.failed || !ok)) atomicOr(p.status, STATUS_TIMEOUT);
+        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
+        return;
+    }
+
+    // ---- compute warps: S^T = K Q^T for the warp's 16 keys, O^T += V^T P^T.  Thread
+    // (g, tq) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and query rows 2 tq,
+    // 2 tq + 1 (+ 8 per row tile).
+    const int g = lane >> 2, tq = lane & 3;
+    int tok[NR][2];      // the token of each of the thread's rows
+    bool rvalid[NR][2];
+    int hq_g[NR][2];     // and its head within the group
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * nt + 2 * tq + j;
+            rvalid[nt][j] = r < p.rows;
+            tok[nt][j] = rvalid[nt][j] ? r % p.q_len : 0;
+            hq_g[nt][j] = rvalid[nt][j] ? r / p.q_len : 0;
+        }
+    float slope[NR][2];
+    uint32_t qb[NR][KD][2];
+    auto load_segment = [&](int b, int hk) {
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                slope[nt][j] = SCORE == FA_SCORE_ALIBI ? __ldg(p.slopes + hk * p.G + hq_g[nt][j]) * kLog2e : 0.f;
+            const int rb = 8 * nt + g;  // the B fragment's column
+            const bool vb = rb < p.rows;
+            const int rv = vb ? rb : 0;
+            const uint16_t* src = p.q + (int64_t)b * p.q_st0 + (int64_t)(hk * p.G + rv / p.q_len) * p.q_st1 +
+                                  (int64_t)(rv % p.q_len) * p.q_st2 + 2 * tq;
+#pragma unroll
+            for (int kk = 0; kk < KD; ++kk) {
+                qb[nt][kk][0] = vb ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
+                qb[nt][kk][1] = vb ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
+            }
+        }
+    };
+    float oacc[KD][NR][4];
+    float m_run[NR][2], l_run[NR][2];  // log2 units; l: this thread's keys only
+    auto reset = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oacc[mt][nt][e] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m_run[nt][j] = -INFINITY;
+                l_run[nt][j] = 0.f;
+            }
+    };
+    float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);  // [warp][row][OROW]
+
+    // One output row element group (four columns at d of row r): O / l and LSE.
+    auto write_out = [&](int b, int hk, int r, int d, float M, float L, const float (&v)[4]) {
+        const int hq = hk * p.G + r / p.q_len, i = r % p.q_len;
+        const bool some = L > 0.f && M != -INFINITY;
+        const float inv = some ? 1.0f / L : 0.f;
+        uint16_t* o = p.o + (int64_t)b * p.o_st0 + (int64_t)hq * p.o_st1 + (int64_t)i * p.o_st2 + d;
+        // a row that attends nothing: O = 0
+        *reinterpret_cast<uint2*>(o) =
+            some || L != L ? make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv))
+                           : make_uint2(0u, 0u);
+        if (d == 0 && p.lse)
+            p.lse[((int64_t)b * p.Hq + hq) * p.q_len + i] = some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+    };
+
+    // The end of a piece: the warps' states joined, and the segment written out if
+    // this was its last piece to arrive.
+    auto end_piece = [&](const PdWalk& at, long long xseg) {
+        compute_sync();  // the last piece's states have been read
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float l = l_run[nt][j];  // sum over the eight key groups
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+                if (g == 0) {
+                    sh.m[warp][8 * nt + 2 * tq + j] = m_run[nt][j];
+                    sh.l[warp][8 * nt + 2 * tq + j] = l;
+                }
+                const int r = 8 * nt + 2 * tq + j;
+                float* dst = join + (warp * RMAX + r) * C::OROW + g;
+#pragma unroll
+                for (int mt = 0; mt < KD; ++mt) {
+                    dst[16 * mt] = oacc[mt][nt][j];
+                    dst[16 * mt + 8] = oacc[mt][nt][2 + j];
+                }
+            }
+        compute_sync();
+        const int c0 = pd_holder(T, xseg, used), c1 = pd_holder(T, xseg + at.r.n - 1, used);
+        const int items = p.rows * (D / 4);
+        for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
+            const int r = it / (D / 4), d = (it % (D / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kPdWarps; ++k) M = fmaxf(M, sh.m[k][r]);
+            const float Mu = M == -INFINITY ? 0.f : M;
+            float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kPdWarps; ++k) {
+                const float f = ex2_approx(sh.m[k][r] - Mu);
+                const float4 x = *reinterpret_cast<const float4*>(join + (k * RMAX + r) * C::OROW + d);
+                L = fmaf(sh.l[k][r], f, L);
+                v[0] = fmaf(x.x, f, v[0]);
+                v[1] = fmaf(x.y, f, v[1]);
+                v[2] = fmaf(x.z, f, v[2]);
+                v[3] = fmaf(x.w, f, v[3]);
+            }
+            if (c0 == c1) {
+                write_out(at.b, at.hk, r, d, M, L, v);
+            } else {
+                const int64_t part = (2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x)) * p.rows + r;
+                __stcg(reinterpret_cast<float4*>(p.part_o + part * D + d), make_float4(v[0], v[1], v[2], v[3]));
+                if (d == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + part * 2), make_float2(M, L));
+            }
+        }
+        if (c0 != c1) {
+            __threadfence();
+            compute_sync();
+            if (threadIdx.x == 0) {
+                const unsigned n = (unsigned)(c1 - c0);
+                sh.last = atomicInc(p.arrived + c0, n) == n;  // wraps to zero at the last piece
+                __threadfence();
+            }
+            compute_sync();
+            if (sh.last) {
+                __threadfence();
+                for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
+                    const int r = it / (D / 4), d = (it % (D / 4)) * 4;
+                    float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int c = c0; c <= c1; ++c) {
+                        const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows + r;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + part * 2));
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + part * D + d));
+                        const float Mn = fmaxf(M, ml.x), Mu = Mn == -INFINITY ? 0.f : Mn;
+                        const float a = ex2_approx(M - Mu), f = ex2_approx(ml.x - Mu);
+                        M = Mn;
+                        L = fmaf(ml.y, f, L * a);
+                        v[0] = fmaf(x.x, f, v[0] * a);
+                        v[1] = fmaf(x.y, f, v[1] * a);
+                        v[2] = fmaf(x.z, f, v[2] * a);
+                        v[3] = fmaf(x.w, f, v[3] * a);
+                    }
+                    write_out(at.b, at.hk, r, d, M, L, v);
+                }
+            }
+        }
+    };
+
+    const float F = SCORE == FA_SCORE_SOFTCAP ? p.softcap * kLog2e : p.scale * kLog2e;
+    if (count > 0) load_segment(w.b, w.hk);
+    reset();
+    long long xseg = x0 - w.t;  // list position of the segment's first page
+    for (long long i = 0; i < count; ++i) {
+        PdWalk wn = w;
+        if (i + 1 < count) pd_advance(p, wn, bad);
+        const uint32_t slot = (uint32_t)(i % C::NS), use = (uint32_t)(i / C::NS);
+        // after a timeout the warp still walks its share (without computing), so that
+        // the pieces' barriers and counters stay whole
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[slot], use & 1, wd));
+        if (ok) {
+            const uint32_t kbase = smem_u32(smem + slot * C::STAGE), vbase = kbase + C::TILE;
+            const int key0 = 16 * warp;
+            const int m4 = lane >> 3;
+            const int kv0 = (w.r.lo + w.t) * 128;
+            const int pos0 = w.r.len - p.q_len, pos1 = w.r.len - 1;  // first and last query row's positions
+            // some row does not attend the whole page
+            const bool edge = kv0 + 127 > pos0 || (p.has_window && kv0 < pos1 - p.window);
+
+            constexpr bool kEarly = !(D == 128 && NR == 2);
+            uint32_t ka[kEarly ? KD : 1][4], va[kEarly ? KD : 1][4];
+            if constexpr (kEarly) {
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk)
+                    ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[kk]);
+#pragma unroll
+                for (int mt = 0; mt < KD; ++mt)
+                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[mt]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.empty[slot]);
+            }
+            float sacc[NR][4];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KD; ++kk) {
+                if constexpr (!kEarly)
+                    ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[0]);
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+                    mma_bf16_16816(sacc[nt], ka[kEarly ? kk : 0], qb[nt][kk][0], qb[nt][kk][1]);
+            }
+
+            // score_mod in log2 units; masked scores are replaced
+            float mt_[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) mt_[nt][j] = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = e & 1;
+                    const int kv = kv0 + key0 + g + 8 * (e >> 1);
+                    const int pos = pos0 + tok[nt][j];
+                    bool adm = rvalid[nt][j];
+                    if (edge) adm = adm && kv <= pos && (!p.has_window || (int64_t)pos - kv <= p.window);
+                    float x = sacc[nt][e];
+                    if constexpr (SCORE == FA_SCORE_SOFTCAP) x = tanh_accurate(x * p.softcap_in) * F;
+                    else if constexpr (SCORE == FA_SCORE_ALIBI) x = fmaf(slope[nt][j], (float)(kv - pos), x * F);
+                    else x = x * F;
+                    x = adm ? x : -INFINITY;
+                    sacc[nt][e] = x;
+                    mt_[nt][j] = fmaxf(mt_[nt][j], x);
+                }
+            float alpha[NR][2], m_use[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float m = mt_[nt][j];
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                    const float m_new = fmaxf(m_run[nt][j], m);
+                    m_use[nt][j] = m_new == -INFINITY ? 0.f : m_new;
+                    alpha[nt][j] = ex2_approx(m_run[nt][j] - m_use[nt][j]);  // 0 while nothing was admitted
+                    m_run[nt][j] = m_new;
+                    l_run[nt][j] *= alpha[nt][j];
+                }
+            // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor core's operand
+            // type); the sum is taken of the unrounded values
+            uint32_t pb[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt) {
+                float pv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    pv[e] = ex2_approx(sacc[nt][e] - m_use[nt][e & 1]);
+                    l_run[nt][e & 1] += pv[e];
+                }
+                pb[nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
+                pb[nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
+            }
+#pragma unroll
+            for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
+            if (!edge) {
+#pragma unroll
+                for (int mt = 0; mt < KD; ++mt) {
+                    if constexpr (!kEarly)
+                        ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[0]);
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt)
+                        mma_bf16_16816(oacc[mt][nt], va[kEarly ? mt : 0], pb[nt][0], pb[nt][1]);
+                }
+            } else {
+                // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the
+                // same + 8 that a row at positions [from, to] may attend
+                auto keep = [&](int from, int to, uint32_t (&k2)[2]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int kv = kv0 + key0 + 2 * tq + 8 * h;
+                        const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
+                        const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
+                        k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
+                    }
+                };
+                uint32_t any2[2];
+                keep(pos0, pos1, any2);
+#pragma unroll
+                for (int mt = 0; mt < KD; ++mt) {
+                    uint32_t vr[4];
+                    if constexpr (!kEarly) {
+                        ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), vr);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) vr[e] = va[mt][e];
+                    }
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        vr[e] &= any2[e >> 1];
+                        odd |= nonfinite2(vr[e]);
+                    }
+                    if (p.q_len > 1 && __any_sync(0xFFFFFFFFu, odd)) {
+                        // an infinity or NaN that some rows attend and others may not: one
+                        // product per token, each with its own keys, kept for its rows only
+                        for (int i = 0; i < p.q_len; ++i) {
+                            uint32_t k2[2], vi[4];
+                            keep(pos0 + i, pos0 + i, k2);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) vi[e] = vr[e] & k2[e >> 1];
+#pragma unroll
+                            for (int nt = 0; nt < NR; ++nt) {
+                                float d4[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_bf16_16816(d4, vi, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (tok[nt][e & 1] == i) oacc[mt][nt][e] += d4[e];
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(oacc[mt][nt], vr, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            if constexpr (!kEarly) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.empty[slot]);
+            }
+        }
+        // the piece ends with the segment or with the share
+        if (i + 1 == count || wn.t == 0) {
+            end_piece(w, xseg);
+            if (i + 1 < count) {
+                xseg += w.r.n;
+                load_segment(wn.b, wn.hk);
+                reset();
+            }
+        }
+        w = wn;
+    }
+    // sequences without a key: O = 0, LSE = -inf
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (pd_range(p, __ldg(p.seq_lens + b), bad).n > 0) continue;
+        const int per_head = p.q_len * (D / 8);
+        for (int it = threadIdx.x; it < p.Hq * per_head; it += 32 * kPdWarps) {
+            const int h = it / per_head, i = it % per_head / (D / 8), u = it % (D / 8);
+            uint16_t* o = p.o + (int64_t)b * p.o_st0 + (int64_t)h * p.o_st1 + (int64_t)i * p.o_st2;
+            reinterpret_cast<uint4*>(o)[u] = make_uint4(0, 0, 0, 0);
+            if (u == 0 && p.lse) p.lse[((int64_t)b * p.Hq + h) * p.q_len + i] = -INFINITY;
+        }
+    }
+    if (bad && threadIdx.x < 32 * kPdWarps) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
+    if (wd.failed && lane == 0) atomicOr(p.status, STATUS_TIMEOUT);
+}
+
+template <int D, int SCORE, int NR>
+cudaError_t launch_variant(const PdParams& p, cudaStream_t stream)
+{
+    static std::mutex mu;
+    static std::vector<CtxKey> done;
+    auto kern = paged_decode_kernel<D, SCORE, NR>;
+    {
+        CtxKey key;
+        std::lock_guard<std::mutex> lock(mu);
+        bool have = false;
+        if (current_ctx(&key))
+            for (const CtxKey& k : done) have |= k == key;
+        if (!have) {
+            cudaError_t e =
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<D, NR>::SMEM);
+            if (e != cudaSuccess) return e;
+            if (current_ctx(&key)) done.push_back(key);
+        }
+    }
+    kern<<<(unsigned)p.grid, kPdThreads, PdCfg<D, NR>::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_paged_decode(const PdParams& p, int D, int score_kind, cudaStream_t stream)
+{
+#define FA_PD_CASE(DD, SS)                    \
+    if (D == DD && score_kind == SS)          \
+        return p.rows > 8 ? launch_variant<DD, SS, 2>(p, stream) : launch_variant<DD, SS, 1>(p, stream);
+    FA_PD_CASE(64, FA_SCORE_NONE) FA_PD_CASE(64, FA_SCORE_ALIBI) FA_PD_CASE(64, FA_SCORE_SOFTCAP)
+    FA_PD_CASE(128, FA_SCORE_NONE) FA_PD_CASE(128, FA_SCORE_ALIBI) FA_PD_CASE(128, FA_SCORE_SOFTCAP)
+#undef FA_PD_CASE
+    return cudaErrorInvalidValue;
+}
+
+} // namespace fa

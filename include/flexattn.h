@@ -329,6 +329,150 @@ int fa_decode(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const 
               const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse, void* workspace,
               size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ paged cache: filling and decoding */
+
+/* Rotary positions.  The element pairs of a head's first `rotary_dim` elements are
+ * turned by the angle position * inv_freq[j]:
+ *   a' = amplitude (a cos - b sin),   b' = amplitude (b cos + a sin)
+ * where pair j is elements (j, j + rotary_dim / 2) in the half layout and
+ * (2 j, 2 j + 1) in the interleaved one; the head's other elements are copied.  The
+ * angle is formed and reduced in 64 bits, so far positions keep their accuracy. */
+typedef struct fa_rope {
+    const double* inv_freq;           /* device fp64 [rotary_dim / 2]: radians per position */
+    int32_t rotary_dim;               /* a multiple of 16, 0 (nothing is turned) to D */
+    int32_t interleaved;              /* 0: half layout, else interleaved pairs */
+    float amplitude;                  /* multiplies the turned elements; 0 means 1 */
+} fa_rope;
+
+typedef enum fa_rope_scaling_kind {
+    FA_ROPE_UNSCALED = 0,  /* f_j = base^(-2 j / rotary_dim) */
+    FA_ROPE_LINEAR = 1,    /* f_j / factor: positions interpolated */
+    FA_ROPE_BASE = 2,      /* base * factor^(r / (r - 2)), r = rotary_dim: the lowest frequency
+                              divided by factor, the highest kept */
+    FA_ROPE_BANDS = 3,     /* frequencies that turn more than rot_hi times over original_len
+                              positions kept, less than rot_lo times divided by factor, in between
+                              interpolated over the number of turns */
+    FA_ROPE_YARN = 4       /* the same idea, interpolated over the pair's index between those of
+                              rot_hi and rot_lo turns (rounded outwards), and amplitude
+                              0.1 ln(factor) + 1 */
+} fa_rope_scaling_kind;
+
+/* How frequencies are stretched for contexts longer than original_len. */
+typedef struct fa_rope_scaling {
+    int32_t kind;                     /* fa_rope_scaling_kind */
+    double factor;                    /* >= 1 */
+    double original_len;              /* BANDS, YARN: > 0 */
+    double rot_lo, rot_hi;            /* BANDS, YARN: 0 < rot_lo < rot_hi (turns over original_len) */
+} fa_rope_scaling;
+
+/* Frequencies of rotary positions, on the HOST: inv_freq [rotary_dim / 2] (fp64) and
+ * the amplitude (may be NULL).  scaling NULL means FA_ROPE_UNSCALED.  Pure host
+ * arithmetic; copy inv_freq to the device for the calls below.
+ * Errors: FA_ERR_INVALID_ARG for rotary_dim not a positive even number, base <= 1, an
+ * unknown kind or parameters outside the ranges above (BASE needs rotary_dim > 2). */
+int fa_rope_frequencies(int rotary_dim, double base, const fa_rope_scaling* scaling, double* inv_freq,
+                        float* amplitude);
+
+/* Rotary positions on Q and K (either may be NULL with its output) in one launch.
+ *
+ * In:  q [B, Hq, S, D], k [B, Hk, S, D] (bf16, fa_tensor layout rules; D in {64, 128}).
+ *      positions: device int32, token (b, s) at positions[b * positions_stride + s]
+ *      (positions_stride = 0 shares one row); NULL means position_offset + s.
+ *      inverse != 0 turns by the negated angle: applied to the gradients of q_out and
+ *      k_out it gives those of q and k (the amplitude multiplies them too).
+ * Out: q_out, k_out of the inputs' shapes.  An output may be its own input (same data
+ *      and strides); any other overlap is not allowed.
+ * Errors: FA_ERR_INVALID_ARG for shapes that differ, a NULL inv_freq with
+ * rotary_dim > 0, rotary_dim > D, an amplitude that is negative or not finite;
+ * FA_ERR_UNSUPPORTED for another D or a rotary_dim that is not a multiple of 16. */
+int fa_rope_apply(const fa_tensor* q, const fa_tensor* k, const fa_rope* rope, const int32_t* positions,
+                  int64_t positions_stride, int64_t position_offset, int inverse, const fa_tensor* q_out,
+                  const fa_tensor* k_out, void* stream);
+
+/* Append new keys and values to a paged cache, K (and Q) rotated on the way.
+ *
+ * Token s of sequence b has position p = cache_lens[b] + s; its key (rotated) and value
+ * go to slot p % FA_BLOCK_SIZE of page page_table[b * page_table_stride + p /
+ * FA_BLOCK_SIZE], and its query (rotated) to q_out.
+ *
+ * In:  k, v [B, Hkv, S, D] bf16 (token-major views are fine); q [B, Hq, S, D] or NULL.
+ *      rope: NULL or rotary_dim = 0 means no rotation.
+ *      cache_lens: device int32 [B], the cached keys before the call (it is not
+ *      changed).  new_lens: device int32 [B] or NULL (= S for every sequence): only
+ *      tokens s < new_lens[b] are appended; the others' places in the pools and rows of
+ *      q_out are left as they were.
+ *      page_table: device int32 [B, pages_per_seq], rows page_table_stride apart, only
+ *      the entries of pages that new tokens fall into are read.
+ *      workspace: the status word, >= fa_workspace_size() bytes.
+ * Out: k_pages, v_pages [num_pages, Hkv, FA_BLOCK_SIZE, D], the new tokens' slots;
+ *      q_out [B, Hq, S, D] (NULL when q is; may be q itself).
+ * Two new tokens must not fall into the same slot (sequences that share a page do not
+ * append to it): which one stays there is not defined.
+ * Errors: FA_ERR_INVALID_ARG / FA_ERR_UNSUPPORTED as fa_rope_apply and
+ * fa_forward_paged.  Reported as FA_ERR_BAD_BLOCKMASK by fa_get_device_status: a
+ * negative cache_lens or new_lens (nothing is appended to that sequence), a new_lens
+ * above S (taken as S), a position past pages_per_seq pages or a page outside
+ * [0, num_pages) (such tokens are left out, q_out included). */
+int fa_paged_append(const fa_tensor* k, const fa_tensor* v, const fa_tensor* q, const fa_rope* rope,
+                    const int32_t* cache_lens, const int32_t* new_lens, const int32_t* page_table,
+                    int64_t page_table_stride, int64_t pages_per_seq, const fa_tensor* k_pages,
+                    const fa_tensor* v_pages, const fa_tensor* q_out, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Bytes of device workspace fa_decode_paged needs (status word, a counter and two
+ * partial results per SM).  Does not depend on the batch or the cache's length, but on
+ * the SM count of the current device. */
+size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D);
+
+/* FlexDecoding over a paged cache: the forward pass for a few query tokens per
+ * sequence, every sequence with its own length (paper review sec. 3.1 and 4.5).
+ *
+ * Query token i of sequence b sits at position seq_lens[b] - q_len + i and attends the
+ * cached keys at positions <= its own and, with window >= 0, >= its own - window (the
+ * SLIDING leaf).  The q_len newest keys are in the cache already (fa_paged_append).
+ *
+ * In:  q [B, Hq, q_len, D], (Hq / Hkv) * q_len <= 16; k_pages, v_pages
+ *      [num_pages, Hkv, FA_BLOCK_SIZE, D]; page_table int32 [B, pages_per_seq], rows
+ *      page_table_stride apart; seq_lens device int32 [B], the new tokens included.
+ *      Pages may be shared between sequences.  Whatever the places behind a sequence's
+ *      last key, or keys a row does not attend, hold (infinities and NaN included) does
+ *      not reach the row.
+ *      window < 0: none.  sm: NONE, ALIBI or SOFTCAP (NULL = none); ALiBi's distance is
+ *      that of the positions.  scale as fa_forward.
+ *      workspace: >= fa_decode_paged_workspace_size(...) bytes, 16-byte aligned, zeroed
+ *      once before its first use; every call leaves it ready for the next, of any
+ *      shape.  Calls that overlap in time need distinct workspaces.
+ * Out: o [B, Hq, q_len, D] bf16, lse fp32 [B, Hq, q_len] or NULL; a row that attends
+ *      nothing (a sequence of length 0, or a query token before its first key) gets
+ *      O = 0, LSE = -inf.  The same inputs give the same bits.
+ * Errors: as fa_decode; FA_ERR_UNSUPPORTED for more than 16 rows per kv head, a bias
+ * score_mod or D.  A length below zero or beyond pages_per_seq pages and a page outside
+ * the pool are clamped (no read outside the pools) and reported as FA_ERR_BAD_BLOCKMASK
+ * by fa_get_device_status. */
+int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
+                    int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
+                    const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace fa_decode_shared needs. */
+size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
+                                       int64_t prefix_len);
+
+/* fa_decode_paged (without a window) for a batch whose sequences share a long prefix:
+ * the first prefix_len / FA_BLOCK_SIZE entries of every row of page_table name the same
+ * pages (a system prompt, the samples of one prompt), and the prefix is taken once for
+ * all sequences.  Same result as fa_decode_paged.
+ *
+ * In:  as fa_decode_paged; prefix_len >= 0, a multiple of FA_BLOCK_SIZE, at most
+ *      pages_per_seq * FA_BLOCK_SIZE.  The shared entries are read from row 0 for the
+ *      sequences whose every query token sits at position >= prefix_len; a shorter
+ *      sequence is taken by itself from its own row.
+ * Errors: as fa_decode_paged; FA_ERR_INVALID_ARG for such a prefix_len. */
+int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,
+                     const int32_t* page_table, int64_t page_table_stride, int64_t pages_per_seq,
+                     const int32_t* seq_lens, int64_t prefix_len, const fa_score_mod* sm, float scale,
+                     const fa_tensor* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then return the device status recorded in `workspace`
  * by earlier fa_forward calls (FA_OK, FA_ERR_TIMEOUT or FA_ERR_BAD_BLOCKMASK) and
  * clear it.  FA_ERR_CUDA if the stream reports an error. */
