@@ -12,6 +12,7 @@
 #include "flexattn.h"
 #include "paged_decode.cuh"
 #include "rope.cuh"
+#include "shared_prefix.cuh"
 
 using fa::aligned16;
 using fa::check_tensor;
@@ -211,13 +212,14 @@ namespace {
 // Workspace of a paged decode: the status word, a counter per CTA, then per partial
 // result (two per CTA) the (running max, sum) and the unnormalised O of every packed
 // query row, each part 256-byte aligned.  The counters lie at the same place for every
-// shape, since they alone must be zero when a call starts.
+// shape, since they alone must be zero when a call starts.  With a shared prefix, the
+// prefix's partial results and every row's own state follow.
 struct PdLayout {
-    size_t arrived, ml, o, end;
-    int sms;
+    size_t arrived, ml, o, pre_ml, pre_o, own_ml, own_o, end;
+    int sms, pre_ctas;  // one CTA per SM; CTAs of the prefix
 };
 
-PdLayout pd_layout(int64_t rows, int64_t D)
+PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
 {
     PdLayout L;
     L.sms = sm_count();
@@ -226,14 +228,28 @@ PdLayout pd_layout(int64_t rows, int64_t D)
     L.ml = L.arrived + align256(ctas * sizeof(uint32_t));
     L.o = L.ml + align256(parts * 2 * sizeof(float));
     L.end = L.o + parts * D * sizeof(float);
+    L.pre_ml = L.pre_o = L.own_ml = L.own_o = 0;
+    L.pre_ctas = 0;
+    if (prefix_pages > 0) {
+        const fa::SpGeom g = fa::sp_geom(B * rows, (int32_t)prefix_pages);
+        const int64_t entries = Hkv * g.per_head;
+        L.pre_ctas = (int)(entries < (int64_t)ctas ? entries : (int64_t)ctas);
+        const size_t slots = 2 * ((size_t)Hkv * fa::sp_cols(g) + L.pre_ctas) * fa::kSpRows;
+        const size_t own = (size_t)(B * Hkv * rows);
+        L.pre_ml = align256(L.end);
+        L.pre_o = L.pre_ml + align256(slots * 2 * sizeof(float));
+        L.own_ml = L.pre_o + slots * D * sizeof(float);
+        L.own_o = L.own_ml + align256(own * 2 * sizeof(float));
+        L.end = L.own_o + own * D * sizeof(float);
+    }
     return L;
 }
 
 // fa_decode_paged and fa_decode_shared (prefix_len > 0).
 int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
                  int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
-                 const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse, void* workspace,
-                 size_t workspace_bytes, void* stream)
+                 int64_t prefix_pages, const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse,
+                 void* workspace, size_t workspace_bytes, void* stream)
 {
     int rc;
     if ((rc = check_tensor(q)) || (rc = check_tensor(o)) || (rc = check_pools(k_pages, v_pages))) return rc;
@@ -255,7 +271,10 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (B * Hq * q_len == 0) return FA_OK;
     if (!seq_lens || (pages_per_seq > 0 && (!page_table || num_pages < 1))) return FA_ERR_INVALID_ARG;
     if (B * Hkv * pages_per_seq > (int64_t(1) << 40)) return FA_ERR_UNSUPPORTED;  // work list positions
-    const PdLayout lay = pd_layout((Hq / Hkv) * q_len, D);
+    // entries of the prefix's list for a head, and its rows
+    if (prefix_pages > 0 && (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
+        return FA_ERR_UNSUPPORTED;
+    const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
     if (lay.sms <= 0) return FA_ERR_CUDA;
     if (workspace_bytes < lay.end) return FA_ERR_INVALID_ARG;
 
@@ -279,6 +298,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.pt_stride = page_table_stride;
     P.pt_width = (int32_t)pages_per_seq;
     P.num_pages = (int32_t)num_pages;
+    P.prefix_pages = (int32_t)prefix_pages;
     P.has_window = window >= 0 ? 1 : 0;
     P.window = window >= 0 ? (window < kMaxLen ? window : kMaxLen) : 0;
     P.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
@@ -295,8 +315,38 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.part_o = reinterpret_cast<float*>(ws + lay.o);
     P.status = reinterpret_cast<int*>(ws);
     P.watchdog_ns = fa::watchdog_ns();
-    return fa::launch_paged_decode(P, (int)D, kind, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
-                                                                                                       : FA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (prefix_pages == 0) return fa::launch_paged_decode(P, (int)D, kind, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+
+    P.own_ml = reinterpret_cast<float*>(ws + lay.own_ml);
+    P.own_o = reinterpret_cast<float*>(ws + lay.own_o);
+    fa::SpParams S;
+    std::memset(&S, 0, sizeof S);
+    S.tm_k = P.tm_k;
+    S.tm_v = P.tm_v;
+    S.q = P.q;
+    S.q_st0 = P.q_st0; S.q_st1 = P.q_st1; S.q_st2 = P.q_st2;
+    S.B = P.B; S.Hkv = P.Hkv; S.G = P.G; S.q_len = P.q_len; S.rows = P.rows;
+    S.seq_lens = seq_lens;
+    S.prefix_row = page_table;
+    S.num_pages = P.num_pages;
+    S.scale = P.scale; S.softcap = P.softcap; S.softcap_in = P.softcap_in;
+    S.slopes = P.slopes;
+    S.geom = fa::sp_geom(B * P.rows, (int32_t)prefix_pages);
+    S.used = lay.pre_ctas;
+    S.part_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
+    S.part_o = reinterpret_cast<float*>(ws + lay.pre_o);
+    S.o = P.o;
+    S.o_st0 = P.o_st0; S.o_st1 = P.o_st1; S.o_st2 = P.o_st2;
+    S.lse = lse;
+    S.own_o = P.own_o;
+    S.own_ml = P.own_ml;
+    S.pt_width = P.pt_width;
+    S.status = P.status;
+    S.watchdog_ns = P.watchdog_ns;
+    if (fa::launch_shared_prefix(S, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
+    if (fa::launch_paged_decode(P, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
+    return fa::launch_shared_join(S, (int)D, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 } // namespace
@@ -307,7 +357,7 @@ size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_
 {
     if (B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
-    return pd_layout((Hq / Hkv) * q_len, D).end;
+    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, 0).end;
 }
 
 int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
@@ -315,15 +365,16 @@ int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tenso
                     const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream)
 {
-    return decode_paged(q, k_pages, v_pages, page_table, page_table_stride, pages_per_seq, seq_lens, window, sm, scale,
-                        o, lse, workspace, workspace_bytes, stream);
+    return decode_paged(q, k_pages, v_pages, page_table, page_table_stride, pages_per_seq, seq_lens, window, 0, sm,
+                        scale, o, lse, workspace, workspace_bytes, stream);
 }
 
 size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
                                        int64_t prefix_len)
 {
-    if (prefix_len < 0) return 0;
-    return fa_decode_paged_workspace_size(B, Hq, Hkv, q_len, D);
+    if (prefix_len < 0 || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
+    if (B * Hq * q_len == 0) return kWorkspaceBytes;
+    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_len / FA_BLOCK_SIZE).end;
 }
 
 int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,
@@ -333,8 +384,8 @@ int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tens
 {
     if (prefix_len < 0 || prefix_len % FA_BLOCK_SIZE != 0) return FA_ERR_INVALID_ARG;
     if (prefix_len / FA_BLOCK_SIZE > pages_per_seq) return FA_ERR_INVALID_ARG;
-    return decode_paged(q, k_pages, v_pages, page_table, page_table_stride, pages_per_seq, seq_lens, -1, sm, scale, o,
-                        lse, workspace, workspace_bytes, stream);
+    return decode_paged(q, k_pages, v_pages, page_table, page_table_stride, pages_per_seq, seq_lens, -1,
+                        prefix_len / FA_BLOCK_SIZE, sm, scale, o, lse, workspace, workspace_bytes, stream);
 }
 
 } // extern "C"

@@ -1,0 +1,25 @@
+// Launch of a kernel whose CTAs may start before the stream's previous kernel has ended
+// (programmatic dependent launch): the kernel itself waits where it has to.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace fa {
+
+template <class P>
+inline cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, P p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+} // namespace fa

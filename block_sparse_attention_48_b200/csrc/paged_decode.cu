@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include "context.cuh"
+#include "dependent_launch.cuh"
 #include "flex_fwd.cuh"
 #include "flexattn.h"
 #include "paged_decode.cuh"
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     bool bad = false;
     Watchdog wd{p.watchdog_ns, false};
+    launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
         if (lane == 0 && (wd.failed || !ok)) atomicOr(p.status, STATUS_TIMEOUT);
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
+        wait_prerequisites();
         return;
     }
 
@@ -252,8 +255,15 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     };
     float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);  // [warp][row][OROW]
 
-    // One output row element group (four columns at d of row r): O / l and LSE.
-    auto write_out = [&](int b, int hk, int r, int d, float M, float L, const float (&v)[4]) {
+    // One output row element group (four columns at d of row r): O / l and LSE, or the
+    // state that joins the shared prefix's.
+    auto write_out = [&](int b, int hk, int r, int d, bool shared, float M, float L, const float (&v)[4]) {
+        if (shared) {
+            const int64_t row = ((int64_t)b * p.Hkv + hk) * p.rows + r;
+            *reinterpret_cast<float4*>(p.own_o + row * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+            if (d == 0) *reinterpret_cast<float2*>(p.own_ml + row * 2) = make_float2(M, L);
+            return;
+        }
         const int hq = hk * p.G + r / p.q_len, i = r % p.q_len;
         const bool some = L > 0.f && M != -INFINITY;
         const float inv = some ? 1.0f / L : 0.f;
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 v[3] = fmaf(x.w, f, v[3]);
             }
             if (c0 == c1) {
-                write_out(at.b, at.hk, r, d, M, L, v);
+                write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
             } else {
                 const int64_t part = (2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x)) * p.rows + r;
                 __stcg(reinterpret_cast<float4*>(p.part_o + part * D + d), make_float4(v[0], v[1], v[2], v[3]));
@@ -345,7 +355,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                         v[2] = fmaf(x.z, f, v[2] * a);
                         v[3] = fmaf(x.w, f, v[3] * a);
                     }
-                    write_out(at.b, at.hk, r, d, M, L, v);
+                    write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
                 }
             }
         }
@@ -545,6 +555,9 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     }
     if (bad && threadIdx.x < 32 * kPdWarps) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
     if (wd.failed && lane == 0) atomicOr(p.status, STATUS_TIMEOUT);
+    // behind a shared prefix's kernel: this grid does not end before it, so that the join
+    // finds both done
+    wait_prerequisites();
 }
 
 template <int D, int SCORE, int NR>
@@ -566,6 +579,8 @@ cudaError_t launch_variant(const PdParams& p, cudaStream_t stream)
             if (current_ctx(&key)) done.push_back(key);
         }
     }
+    if (p.prefix_pages > 0)  // beside the prefix's last CTAs
+        return launch_after(kern, dim3((unsigned)p.grid), kPdThreads, PdCfg<D, NR>::SMEM, stream, p);
     kern<<<(unsigned)p.grid, kPdThreads, PdCfg<D, NR>::SMEM, stream>>>(p);
     return cudaGetLastError();
 }

@@ -44,6 +44,11 @@ struct PdParams {
     unsigned* arrived;    // [grid] pieces done of the segment whose first piece ends share c0;
                           // every call leaves zeros
 
+    // With a shared prefix: the state (log2 max, sum, unnormalised O) of the rows whose
+    // prefix is taken elsewhere, for the join
+    float* own_o;         // [B][Hkv][rows][D] fp32
+    float* own_ml;        // [B][Hkv][rows][2]
+
     int* status;
     uint64_t watchdog_ns;
 };

@@ -1,5 +1,5 @@
 // Host build of the paged decode kernel's walk over its work list
-// (csrc/paged_walk.cuh), for CPU unit tests: the device qualifiers are defined away
+// (csrc/paged_walk.cuh) and of the shared prefix's (csrc/shared_walk.cuh), for CPU unit tests: the device qualifiers are defined away
 // and __ldg becomes a plain load.
 #include <cstdint>
 
@@ -12,6 +12,7 @@ static inline T __ldg(const T* p)
 }
 
 #include "paged_walk.cuh"
+#include "shared_walk.cuh"
 
 namespace {
 
@@ -79,4 +80,35 @@ extern "C" int fa_host_pd_page(int page, int num_pages, int32_t* bad)
     const int r = fa::pd_page(page, num_pages, b);
     *bad = b;
     return r;
+}
+
+// out = (pairs, single, per_head).
+extern "C" void fa_host_sp_geom(long long R, int32_t pages, int32_t* out)
+{
+    const fa::SpGeom g = fa::sp_geom(R, pages);
+    out[0] = g.pairs;
+    out[1] = g.single;
+    out[2] = g.per_head;
+}
+
+// CTA c's pieces: out rows of (hk, col, e0, n, one, tiles of stream 0, of stream 1).
+extern "C" int fa_host_sp_pieces(long long R, int32_t pages, int32_t Hkv, int c, int used, int32_t* out)
+{
+    const fa::SpGeom g = fa::sp_geom(R, pages);
+    const long long T = (long long)Hkv * g.per_head, x1 = fa::pd_share(T, c + 1, used);
+    int n = 0;
+    for (long long x = fa::pd_share(T, c, used); x < x1; ++n) {
+        const fa::SpPiece p = fa::sp_piece(g, x, x1);
+        int32_t* o = out + 7 * n;
+        o[0] = p.hk;
+        o[1] = p.col;
+        o[2] = p.e0;
+        o[3] = p.n;
+        o[4] = p.one;
+        o[5] = fa::sp_tiles(g, p, 0);
+        o[6] = fa::sp_tiles(g, p, 1);
+        if (fa::sp_start(g, p.hk, p.col) + p.e0 != x) return -1;
+        x += p.n;
+    }
+    return n;
 }

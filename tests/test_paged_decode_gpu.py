@@ -213,6 +213,17 @@ def test_decode_shared_with_short_sequences():
     assert_decode(got, ref)
 
 
+def test_decode_shared_reads_the_prefix_from_row_zero():
+    """Every long sequence's prefix is that of row 0 of the table."""
+    fa = _fa()
+    lens = [300, 400]
+    q, k, v, table, sl = paged_case(lens, 1, 4, 2, 64, seed=8, prefix=256)
+    ref = decode_ref(q, k, v, table, lens)
+    tab = table.clone()
+    tab[1, :2] = 0
+    assert_decode(fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), tab.cuda(), sl.cuda(), 256), ref)
+
+
 def test_decode_shared_large_scores():
     """Scores that grow along the prefix by far more than one rescaling step, at an
     explicit scale."""

@@ -205,6 +205,8 @@ def lib():
     L.fa_host_pd_walk.restype = i64
     L.fa_host_pd_holder.argtypes = [i64, i64, ctypes.c_int]
     L.fa_host_pd_page.argtypes = [ctypes.c_int, ctypes.c_int, I32P]
+    L.fa_host_sp_geom.argtypes = [i64, i32, I32P]
+    L.fa_host_sp_pieces.argtypes = [i64, i32, i32, ctypes.c_int, ctypes.c_int, I32P]
     return L
 
 
@@ -285,6 +287,51 @@ def test_pages_are_clamped(lib):
     for page, num, want in ((0, 1, 0), (4, 5, 4), (5, 5, 4), (-1, 5, 0), (2 ** 31 - 1, 7, 6), (-2 ** 31, 7, 0)):
         assert lib.fa_host_pd_page(page, num, ctypes.byref(bad)) == want
         assert bad.value == (page < 0 or page >= num)
+
+
+@pytest.mark.parametrize("R", [1, 16, 127, 128, 129, 255, 256, 257, 384, 385, 512, 2048, 2100])
+@pytest.mark.parametrize("pages", [1, 2, 3, 8, 41])
+@pytest.mark.parametrize("Hkv", [1, 3])
+def test_shared_prefix_work_list(lib, R, pages, Hkv):
+    """Every tile of rows meets every page of the prefix once, in order, and the partial
+    results of a column are those of the CTAs from the holder of its first entry to the
+    holder of its last."""
+    geom = np.zeros(3, np.int32)
+    lib.fa_host_sp_geom(R, pages, geom.ctypes.data_as(I32P))
+    pairs, single, per_head = geom.tolist()
+    tiles = (R + 127) // 128
+    assert 2 * pairs + single in (tiles, tiles + 1) and 256 * pairs + 128 * single >= R
+    T = Hkv * per_head
+    for used in {1, min(T, 7), min(T, 148)}:
+        seen, slots, holders = {}, set(), {}
+        out = np.zeros(7 * (T + 1), np.int32)
+        for c in range(used):
+            n = lib.fa_host_sp_pieces(R, pages, Hkv, c, used, out.ctypes.data_as(I32P))
+            assert n > 0
+            for hk, col, e0, m, one, t0, t1 in out[:7 * n].reshape(n, 7).tolist():
+                assert m > 0
+                for s in (0, 1):
+                    slot = 2 * (hk * (pairs + single) + col + c) + s
+                    assert slot not in slots and slot < 2 * (Hkv * (pairs + single) + used)
+                    slots.add(slot)
+                holders.setdefault((hk, col), []).append(c)
+                for s, t in ((0, t0), (1, t1)):
+                    for e in range(e0, e0 + t):
+                        tile, page = (2 * col, 2 * e + s) if one else (2 * col + s, e)
+                        seen.setdefault((hk, tile), []).append(page)
+        for hk in range(Hkv):
+            for tile in range(tiles):
+                # a column of one tile alternates between its streams within a piece
+                got = seen[(hk, tile)]
+                assert sorted(got) == list(range(pages))
+                if tile < 2 * pairs:
+                    assert got == sorted(got)
+            for col in range(pairs + single):
+                start = hk * per_head + col * pages
+                n = pages if col < pairs else (pages + 1) // 2
+                c0 = lib.fa_host_pd_holder(T, start, used)
+                c1 = lib.fa_host_pd_holder(T, start + n - 1, used)
+                assert holders[(hk, col)] == list(range(c0, c1 + 1))
 
 
 def test_workspace_sizes():
