@@ -533,10 +533,10 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
         // the piece ends with the segment or with the share
         if (i + 1 == count || wn.t == 0) {
+            if (i + 1 < count) load_segment(wn.b, wn.hk);  // its latency passes during the join
             end_piece(w, xseg);
             if (i + 1 < count) {
                 xseg += w.r.n;
-                load_segment(wn.b, wn.hk);
                 reset();
             }
         }

@@ -11,10 +11,13 @@
 // (few rows) to the tensor cores and the exponentials (4 D flops and one exponential per
 // row and key).  A CTA per SM takes an equal share of the list of column entries
 // (shared_walk.cuh).  K and V tiles arrive by TMA in one ring.  Two streams, each a tile
-// of 128 rows with its own MMA warp and four softmax warps, run half a step apart: while
-// one's scores are exponentiated, the other's products are on the tensor cores.  S, P
-// (over S) and O live in tensor memory; a thread owns a row.  No key of the prefix is
-// masked.  The running maximum moves only when a tile exceeds it by 2^8, so that O is
+// of 128 rows with its own MMA warp and four softmax warps, share the tensor cores and
+// the exponential units.  S, P (over S) and O live in tensor memory; a thread owns a
+// row.  A tile is taken in halves of 64 keys with a buffer each: while one half's scores
+// are exponentiated, the other's P V and the scores of the half after it are on the
+// tensor cores (whole tiles, whose P V and next scores wait for the exponentials: 4280
+// cycles per pair of tiles, of which the products need 2050).  No key of the prefix is
+// masked.  The running maximum moves only when a half exceeds it by 2^8, so that O is
 // rarely rescaled.
 #include <mutex>
 #include <vector>
@@ -47,13 +50,13 @@ struct SpCfg {
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int SMEM = OFF_RING + NS * TILE + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory beyond 227 KB per CTA");
-    static constexpr uint32_t s_col(int s) { return 128u * s; }   // S, and P over it
+    static constexpr uint32_t s_col(int s, int h) { return 128u * s + 64u * h; }  // S of 64 keys, and P over it
     static constexpr uint32_t o_col(int s) { return 256u + 128u * s; }
 };
 
 struct __align__(16) SpShared {
     uint64_t full[12], empty[12];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_empty[2], drain[2];
     uint32_t tmem_base;
 };
 
@@ -137,9 +140,9 @@ __device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8
 
 __device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; }
 
-template <int D>
-__device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_t* smem, uint32_t tmem, int s,
-                                         long long x0, long long x1, Watchdog& wd)
+template <int D, int s>
+__device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_t* smem, uint32_t tmem, long long x0,
+                                         long long x1, Watchdog& wd)
 {
     using C = SpCfg<D>;
     const uint32_t hi_k = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
@@ -147,52 +150,76 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
     const uint32_t qd = (uint32_t)sdesc_sw128(smem_u32(smem + s * C::TILE), 16, 1024);
     const uint32_t k0 = (uint32_t)sdesc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
     const uint32_t v0 = (uint32_t)sdesc_sw128(smem_u32(smem + C::OFF_RING), kBox, 1024);
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t kHalf = 8192 >> 4;  // 64 keys of a 64-column box, in descriptor units
     uint32_t at = 0, tile = 0, piece = 0;
-    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, wd)); };
     bool ok = true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+        return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, wd));
+    };
+    // A slot is free after two arrivals: one of each stream, or both of the one that reads it
+    auto release = [&](uint32_t slot, bool one) {
+        umma_commit(&sh.empty[slot]);
+        if (one) umma_commit(&sh.empty[slot]);
+    };
+    // S of one half of a tile whose K has landed
+    auto scores = [&](uint32_t kpos, int h, bool one) {
+        const uint32_t slot = kpos % C::NS, kd = k0 + slot * (uint32_t)(C::TILE >> 4) + h * kHalf;
+        tc_fence_after();
+        if (elect_one_sync()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // 32 bytes per K step inside a 128-byte row, 16 KB per 64 columns
+                const uint32_t off = (uint32_t)(((k / 4) * kBox + (k % 4) * 32) >> 4);
+                umma_ss(tmem + C::s_col(s, h), desc64(hi_k, qd + off), desc64(hi_k, kd + off), idesc_s, k > 0);
+            }
+            umma_commit(&sh.s_full[s][h]);
+            if (h == 1) release(slot, one);
+        }
+        __syncwarp();
+    };
+    // O += P V of one half
+    auto values = [&](uint32_t vpos, int h, bool one, uint32_t accumulate) {
+        const uint32_t slot = vpos % C::NS, vd = v0 + slot * (uint32_t)(C::TILE >> 4) + h * kHalf;
+        tc_fence_after();
+        if (elect_one_sync()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 keys (2 KB of V) per K step
+                umma_ts(tmem + C::o_col(s), tmem + C::s_col(s, h) + 8 * k, desc64(hi_mn, vd + (uint32_t)(k * 128)),
+                        idesc_o, k > 0 ? 1u : accumulate);
+            umma_commit(&sh.pv_done[s]);
+            if (h == 1) release(slot, one);
+        }
+        __syncwarp();
+    };
     for (long long x = x0; ok && x < x1;) {
         const SpPiece pc = sp_piece(p.geom, x, x1);
         const int n = sp_tiles(p.geom, pc, s);
-        if (n > 0) ok = ready(&sh.q_full[s], piece & 1);
-        for (int i = 0; ok && i < n; ++i, ++tile) {
-            const SpSeq q = entry_seq(p.geom, pc, pc.e0 + i, s, at);
-            at += entry_tiles(p.geom, pc, pc.e0 + i);
-            const uint32_t ks = q.k % C::NS, vs = q.v % C::NS;
-            if (!(ok = ready(&sh.full[ks], (q.k / C::NS) & 1))) break;
-            tc_fence_after();
-            if (elect_one_sync()) {
-                const uint32_t kd = k0 + ks * (uint32_t)(C::TILE >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    // 32 bytes per K step inside a 128-byte row, 16 KB per 64 columns
-                    const uint32_t off = (uint32_t)(((k / 4) * kBox + (k % 4) * 32) >> 4);
-                    umma_ss(tmem + C::s_col(s), desc64(hi_k, qd + off), desc64(hi_k, kd + off), idesc_s, k > 0);
-                }
-                umma_commit(&sh.empty[ks]);  // two arrivals free a slot: one of each stream, or
-                if (pc.one) umma_commit(&sh.empty[ks]);  // both of the one that reads it
-                umma_commit(&sh.s_full[s]);
+        if (n > 0) {
+            SpSeq cur = entry_seq(p.geom, pc, pc.e0, s, at);
+            if (ready(&sh.q_full[s], piece & 1) && ready(&sh.full[cur.k % C::NS], (cur.k / C::NS) & 1)) {
+                scores(cur.k, 0, pc.one);
+                scores(cur.k, 1, pc.one);
             }
-            __syncwarp();
-            if (!(ok = ready(&sh.p_full[s], tile & 1))) break;
-            if (i == 0 && piece > 0 && !(ok = ready(&sh.o_empty[s], (piece - 1) & 1))) break;
-            if (!(ok = ready(&sh.full[vs], (q.v / C::NS) & 1))) break;
-            tc_fence_after();
-            if (elect_one_sync()) {
-                const uint32_t vd = v0 + vs * (uint32_t)(C::TILE >> 4);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 keys (2 KB of V) per K step
-                    umma_ts(tmem + C::o_col(s), tmem + C::s_col(s) + 8 * k, desc64(hi_mn, vd + (uint32_t)(k * 128)),
-                            idesc_o, (i > 0 || k > 0) ? 1u : 0u);
-                umma_commit(&sh.empty[vs]);
-                if (pc.one) umma_commit(&sh.empty[vs]);
-                if (i + 1 == n) umma_commit(&sh.o_full[s]);
+            for (int i = 0; ok && i < n; ++i, ++tile) {
+                at += entry_tiles(p.geom, pc, pc.e0 + i);
+                const SpSeq nx = entry_seq(p.geom, pc, pc.e0 + i + 1, s, at);
+                const bool more = i + 1 < n;
+                ready(&sh.full[cur.v % C::NS], (cur.v / C::NS) & 1);
+                if (!ready(&sh.p_full[s][0], tile & 1)) break;
+                if (i == 0 && piece > 0 && !ready(&sh.o_empty[s], (piece - 1) & 1)) break;
+                values(cur.v, 0, pc.one, i > 0 ? 1u : 0u);
+                if (more && !ready(&sh.full[nx.k % C::NS], (nx.k / C::NS) & 1)) break;
+                if (more) scores(nx.k, 0, pc.one);
+                if (!ready(&sh.p_full[s][1], tile & 1)) break;
+                values(cur.v, 1, pc.one, 1u);
+                if (more) scores(nx.k, 1, pc.one);
+                cur = nx;
             }
-            __syncwarp();
+            ++piece;
         }
         for (int i = n; i < pc.n; ++i) at += entry_tiles(p.geom, pc, pc.e0 + i);
-        if (n > 0) ++piece;
         x += pc.n;
     }
     // the products in flight end before tensor memory is given back (bounded)
@@ -203,19 +230,19 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
     if ((wd.failed || dw.failed) && threadIdx.x % 32 == 0) atomicOr(p.status, STATUS_TIMEOUT);
 }
 
-// P = exp2(x * F + b) of one row (128 scores) as bf16 to TMEM, and its sum.  P is off by
-// at most 2^-8 of each entry (the tensor cores' operand type); the sum is taken of the
-// unrounded values.
-__device__ __forceinline__ float exp_row(const float (&x)[128], float F, float b, uint32_t p_addr)
+// P = exp2(x * F + b) of half a tile's row (64 scores) as bf16 to TMEM, and its sum.  P is
+// off by at most 2^-8 of each entry (the tensor cores' operand type); the sum is taken of
+// the unrounded values.
+__device__ __forceinline__ float exp_row(const float (&x)[64], float F, float b, uint32_t p_addr)
 {
     const uint64_t F2 = f2_pack(F, F), b2 = f2_pack(b, b);
     uint64_t la = f2_pack(0.f, 0.f), lb = la;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t pk[8];
+    for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = 16 * c + 2 * j;
+        for (int j = 0; j < 16; ++j) {
+            const int e = 32 * c + 2 * j;
             float a0, a1;
             f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), F2, b2), a0, a1);
             const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
@@ -223,22 +250,22 @@ __device__ __forceinline__ float exp_row(const float (&x)[128], float F, float b
             else la = f2_add(la, f2_pack(e0, e1));
             pk[j] = pack_bf16x2(e0, e1);
         }
-        tmem_st8(p_addr + 8 * c, pk);
+        tmem_st16(p_addr + 16 * c, pk);
     }
     float l0, l1;
     f2_unpack(f2_add(la, lb), l0, l1);
     return l0 + l1;
 }
 
-__device__ __forceinline__ float max_row(const float (&x)[128])
+__device__ __forceinline__ float max_row(const float (&x)[64])
 {
     float m[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        m[c] = max3(x[32 * c], x[32 * c + 1], x[32 * c + 2]);
+        m[c] = max3(x[16 * c], x[16 * c + 1], x[16 * c + 2]);
 #pragma unroll
-        for (int j = 3; j < 31; j += 2) m[c] = max3(m[c], x[32 * c + j], x[32 * c + j + 1]);
-        m[c] = fmaxf(m[c], x[32 * c + 31]);
+        for (int j = 3; j < 15; j += 2) m[c] = max3(m[c], x[16 * c + j], x[16 * c + j + 1]);
+        m[c] = fmaxf(m[c], x[16 * c + 15]);
     }
     return max3(m[0], m[1], fmaxf(m[2], m[3]));
 }
@@ -248,9 +275,10 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
                                              long long x0, long long x1, Watchdog& wd)
 {
     using C = SpCfg<D>;
+    constexpr int U = D / 8;  // 16-byte units of a row
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 4, row = 32 * warp + lane;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const uint32_t s_addr = tmem + C::s_col(s) + lanes, o_addr = tmem + C::o_col(s) + lanes;
+    const uint32_t o_addr = tmem + C::o_col(s) + lanes;
     const uint32_t q_base = smem_u32(smem + s * C::TILE);
     uint32_t tile = 0, piece = 0;
     const float F = SCORE == FA_SCORE_SOFTCAP ? p.softcap * kLog2e : SCORE == FA_SCORE_ALIBI ? 1.f : p.scale * kLog2e;
@@ -262,123 +290,138 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
         const long long slot = 2 * (col + blockIdx.x) + s;
         x0p += pc.n;
         float2* ml = reinterpret_cast<float2*>(p.part_ml) + slot * kSpRows + row;
+        float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kSpRows + row;
         if (n == 0) {
             *ml = make_float2(-INFINITY, 0.f);
+            for (int c = 0; c < D / 4; ++c) dst[c * kSpRows] = make_float4(0.f, 0.f, 0.f, 0.f);
             continue;
         }
-        const int first = 2 * kSpRows * pc.col + (pc.one ? 0 : kSpRows * s);  // row of the head
-        // Q tile: 16-byte units, D / 8 lanes a row; rows past the last are zero.  The last
-        // piece's products have read the tile (their scores were waited for).
-#pragma unroll 4
-        for (int k = 0; k < D / 8; ++k) {
-            const int idx = k * 32 + lane, r = 32 * warp + idx / (D / 8), u = idx % (D / 8);
-            const int R = first + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (R < p.geom.rows) {
-                const int b = R / p.rows, j = R % p.rows;
-                v = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_st0 +
-                                                         (int64_t)(pc.hk * p.G + j / p.q_len) * p.q_st1 +
-                                                         (int64_t)(j % p.q_len) * p.q_st2) + u);
-            }
-            sts128(q_base + (uint32_t)((u >> 3) * kBox + r * 128 + (((u & 7) ^ (r & 7)) << 4)), v.x, v.y, v.z, v.w);
+        // Q tile; rows past the last are zero.  The last piece's products have read the
+        // tile (their end was waited for).
+        const int R = 2 * kSpRows * pc.col + (pc.one ? 0 : kSpRows * s) + row;  // the thread's row of the head
+        const bool valid = R < p.geom.rows;
+        const int b = valid ? R / p.rows : 0, j = valid ? R - b * p.rows : 0, g = j / p.q_len, qi = j - g * p.q_len;
+        const unsigned long long mine =
+            valid ? reinterpret_cast<unsigned long long>(p.q + (int64_t)b * p.q_st0 +
+                                                         (int64_t)(pc.hk * p.G + g) * p.q_st1 + (int64_t)qi * p.q_st2)
+                  : 0ull;
+        uint4 v[U];  // all loads in flight at once, ahead of the K and V tiles' traffic
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int idx = k * 32 + lane;
+            const unsigned long long src = __shfl_sync(0xFFFFFFFFu, mine, idx / U);
+            v[k] = src ? __ldg(reinterpret_cast<const uint4*>(src) + idx % U) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int idx = k * 32 + lane, r = 32 * warp + idx / U, u = idx % U;
+            sts128(q_base + (uint32_t)((u >> 3) * kBox + r * 128 + (((u & 7) ^ (r & 7)) << 4)), v[k].x, v[k].y, v[k].z,
+                   v[k].w);
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(&sh.q_full[s]);
 
         float slope2 = 0.f;
         int pos = 0;
-        if (SCORE == FA_SCORE_ALIBI && first + row < p.geom.rows) {
-            const int b = (first + row) / p.rows, j = (first + row) % p.rows;
-            slope2 = __ldg(p.slopes + pc.hk * p.G + j / p.q_len) * kLog2e;
-            pos = __ldg(p.seq_lens + b) - p.q_len + j % p.q_len;
+        if (SCORE == FA_SCORE_ALIBI && valid) {
+            slope2 = __ldg(p.slopes + pc.hk * p.G + g) * kLog2e;
+            pos = __ldg(p.seq_lens + b) - p.q_len + qi;
         }
         float m_run = -INFINITY, l_run = 0.f;
-        for (int i = 0; i < n; ++i, ++tile) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full[s], tile & 1, wd));
-            if (!ok) break;
-            tc_fence_after();
-            float x[128];
-            {
-                uint32_t raw[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[32 * c + j] = __uint_as_float(raw[c][j]);
-            }
-            if constexpr (SCORE == FA_SCORE_ALIBI) {
-                const int e = pc.e0 + i, kv0 = 128 * (pc.one ? 2 * e + s : e);
-                const float f = p.scale * kLog2e, shift = (float)(kv0 - pos) * slope2;
-                const uint64_t f2 = f2_pack(f, f), sl2 = f2_pack(slope2, slope2), sh2 = f2_pack(shift, shift);
-#pragma unroll
-                for (int j = 0; j < 128; j += 2)
-                    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), f2,
-                                     f2_fma(f2_pack((float)j, (float)(j + 1)), sl2, sh2)), x[j], x[j + 1]);
-            }
-            if constexpr (SCORE == FA_SCORE_SOFTCAP) {
-                // tanh: the polynomial, and per element its far form where a warp's 32
-                // columns have one
-                const uint64_t in2 = f2_pack(p.softcap_in, p.softcap_in);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    bool far = false;
-#pragma unroll
-                    for (int j = 32 * c; j < 32 * c + 32; j += 2) {
-                        f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), in2), x[j], x[j + 1]);
-                        far |= fmaxf(fabsf(x[j]), fabsf(x[j + 1])) > kTanhPolyMax;
-                    }
-                    const bool any = __any_sync(0xFFFFFFFFu, far);
-#pragma unroll
-                    for (int j = 32 * c; j < 32 * c + 32; j += 2) {
-                        float t0, t1;
-                        f2_unpack(tanh_poly2(f2_pack(x[j], x[j + 1])), t0, t1);
-                        if (any) {
-                            if (fabsf(x[j]) > kTanhPolyMax) t0 = tanh_far(x[j]);
-                            if (fabsf(x[j + 1]) > kTanhPolyMax) t1 = tanh_far(x[j + 1]);
-                        }
-                        x[j] = t0;
-                        x[j + 1] = t1;
-                    }
-                }
-            }
-            const float m_tile = max_row(x) * F;
-            float alpha = 1.f;
-            bool rescale = false;
-            if (i == 0) {
-                m_run = m_tile;
-            } else if (m_tile > m_run + kRescale) {
-                alpha = ex2_approx(m_run - m_tile);
-                m_run = m_tile;
-                l_run *= alpha;
-                rescale = true;
-            }
-            l_run += exp_row(x, F, m_run == -INFINITY ? 0.f : -m_run, s_addr);
-            if (__any_sync(0xFFFFFFFFu, rescale)) {
-                // O is stable: this tile's scores were issued after the last tile's P V
+        for (int i = 0; ok && i < n; ++i, ++tile) {
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32];
-                    tmem_ld32(o_addr + 32 * c, ov);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t s_addr = tmem + C::s_col(s, h) + lanes;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full[s][h], tile & 1, wd));
+                if (!ok) break;
+                tc_fence_after();
+                float x[64];
+                {
+                    uint32_t raw[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-                    tmem_st32(o_addr + 32 * c, ov);
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[32 * c + k] = __uint_as_float(raw[c][k]);
                 }
+                if constexpr (SCORE == FA_SCORE_ALIBI) {
+                    const int e = pc.e0 + i, kv0 = 128 * (pc.one ? 2 * e + s : e) + 64 * h;
+                    const float f = p.scale * kLog2e, shift = (float)(kv0 - pos) * slope2;
+                    const uint64_t f2 = f2_pack(f, f), sl2 = f2_pack(slope2, slope2), sh2 = f2_pack(shift, shift);
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2)
+                        f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), f2,
+                                         f2_fma(f2_pack((float)k, (float)(k + 1)), sl2, sh2)), x[k], x[k + 1]);
+                }
+                if constexpr (SCORE == FA_SCORE_SOFTCAP) {
+                    // tanh: the polynomial, and per element its far form where a warp's 32
+                    // columns have one
+                    const uint64_t in2 = f2_pack(p.softcap_in, p.softcap_in);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        bool far = false;
+#pragma unroll
+                        for (int k = 32 * c; k < 32 * c + 32; k += 2) {
+                            f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), in2), x[k], x[k + 1]);
+                            far |= fmaxf(fabsf(x[k]), fabsf(x[k + 1])) > kTanhPolyMax;
+                        }
+                        const bool any = __any_sync(0xFFFFFFFFu, far);
+#pragma unroll
+                        for (int k = 32 * c; k < 32 * c + 32; k += 2) {
+                            float t0, t1;
+                            f2_unpack(tanh_poly2(f2_pack(x[k], x[k + 1])), t0, t1);
+                            if (any) {
+                                if (fabsf(x[k]) > kTanhPolyMax) t0 = tanh_far(x[k]);
+                                if (fabsf(x[k + 1]) > kTanhPolyMax) t1 = tanh_far(x[k + 1]);
+                            }
+                            x[k] = t0;
+                            x[k + 1] = t1;
+                        }
+                    }
+                }
+                const float m_half = max_row(x) * F;
+                float alpha = 1.f;
+                bool rescale = false;
+                if (i == 0 && h == 0) {
+                    m_run = m_half;
+                } else if (m_half > m_run + kRescale) {
+                    alpha = ex2_approx(m_run - m_half);
+                    m_run = m_half;
+                    l_run *= alpha;
+                    rescale = true;
+                }
+                l_run += exp_row(x, F, m_run == -INFINITY ? 0.f : -m_run, s_addr);
+                if (__any_sync(0xFFFFFFFFu, rescale)) {
+                    // O is stable once the P V before this half's is done.  The phase before
+                    // that one has ended: this half's scores were issued after its P V.
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile + h - 1) & 1, wd));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(o_addr + 32 * c, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                        tmem_st32(o_addr + 32 * c, ov);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(&sh.p_full[s][h]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive_warp(&sh.p_full[s]);
         }
         if (!ok) break;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_full[s], piece & 1, wd));
+        // the piece's last P V (and so all its products)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 1) & 1, wd));
         if (!ok) break;
         ++piece;
         tc_fence_after();
         *ml = make_float2(m_run, l_run);
-        float4* dst = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 8) * kSpRows + row) * 2;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
             tmem_ld32(o_addr + 32 * c, ov);
@@ -389,9 +432,8 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                dst[((4 * c + u / 2) * kSpRows) * 2 + u % 2] =
-                    make_float4(__uint_as_float(ov[4 * u]), __uint_as_float(ov[4 * u + 1]),
-                                __uint_as_float(ov[4 * u + 2]), __uint_as_float(ov[4 * u + 3]));
+                dst[(8 * c + u) * kSpRows] = make_float4(__uint_as_float(ov[4 * u]), __uint_as_float(ov[4 * u + 1]),
+                                                         __uint_as_float(ov[4 * u + 2]), __uint_as_float(ov[4 * u + 3]));
         }
     }
     if (wd.failed && lane == 0) atomicOr(p.status, STATUS_TIMEOUT);
@@ -413,9 +455,11 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.q_full[s], 4);
-            mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.p_full[s], 4);
-            mbar_init(&sh.o_full[s], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh.s_full[s][h], 1);
+                mbar_init(&sh.p_full[s][h], 4);
+            }
+            mbar_init(&sh.pv_done[s], 1);
             mbar_init(&sh.o_empty[s], 4);
             mbar_init(&sh.drain[s], 1);
         }
@@ -434,7 +478,8 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     Watchdog wd{p.watchdog_ns, false};
     if (warp < 8) softmax_role<D, SCORE>(p, sh, smem, tmem, warp / 4, x0, x1, wd);
     else if (warp == kLoadWarp) load_role<D>(p, sh, smem, x0, x1, wd);
-    else mma_role<D>(p, sh, smem, tmem, warp - kMmaWarp, x0, x1, wd);
+    else if (warp == kMmaWarp) mma_role<D, 0>(p, sh, smem, tmem, x0, x1, wd);
+    else mma_role<D, 1>(p, sh, smem, tmem, x0, x1, wd);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -442,61 +487,72 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The join: eight columns of a row a thread.  The prefix's pieces in list order, then the
+// The join: a lane a row and a warp four columns of 32, so that the partial results are
+// read in whole lines.  First the maximum over a row's parts, then their weighted sums:
+// no load waits for another part's.  The prefix's pieces come in list order, then the
 // row's own part, whatever finished first.  Sequences that take no part in the sharing
 // were written by the paged decode.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8, kJoinCols = 4 * kJoinWarps;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ SpParams p)
+__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ SpParams p)
 {
-    wait_prerequisites();
-    const long long t = (long long)blockIdx.x * kJoinThreads + threadIdx.x;
-    const int u = (int)(t % (D / 8));
-    const long long row = t / (D / 8);  // of [B][Hkv][rows]
-    if (row >= (long long)p.B * p.Hkv * p.rows) return;
-    const int j = (int)(row % p.rows), hk = (int)(row / p.rows % p.Hkv), b = (int)(row / p.rows / p.Hkv);
-    const int64_t len = __ldg(p.seq_lens + b);
-    if (len > (int64_t)p.pt_width * 128 ? (int64_t)p.pt_width * 128 - p.q_len < (int64_t)p.geom.pages * 128
-                                        : len - p.q_len < (int64_t)p.geom.pages * 128)
-        return;
-    float M = -INFINITY, L = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    auto take = [&](float2 ml, const float4* o) {
-        if (ml.x == -INFINITY && ml.y == 0.f) return;  // no key (its O may be unwritten)
-        const float4 a = o[0], c = o[1];
-        const float Mn = fmaxf(M, ml.x), Mu = Mn == -INFINITY ? 0.f : Mn;
-        const float f0 = ex2_approx(M - Mu), f1 = ex2_approx(ml.x - Mu);
-        M = Mn;
-        L = fmaf(ml.y, f1, L * f0);
-        const float w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(w[e], f1, v[e] * f0);
-    };
-    const int R = b * p.rows + j, col = R / (2 * kSpRows);
+    __shared__ uint2 out[32][kJoinWarps + 1];
+    __shared__ int64_t where[32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int hk = blockIdx.y, R = blockIdx.x * 32 + lane;
+    const int c4 = blockIdx.z * kJoinWarps + warp;  // the four columns
+    const bool in = R < p.geom.rows;
+    const int b = in ? R / p.rows : 0, j = in ? R - b * p.rows : 0;
+    const int hq = hk * p.G + j / p.q_len, i = j % p.q_len;
+    const int64_t most = (int64_t)p.pt_width * 128, raw = __ldg(p.seq_lens + b), len = raw < most ? raw : most;
+    const bool takes = in && len - p.q_len >= (int64_t)p.geom.pages * 128;
+    const int col = R / (2 * kSpRows), r = R % kSpRows;  // the same column and tile in all lanes
     const bool one = col >= p.geom.pairs;
-    const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows, s1 = one ? 1 : s0;
+    const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows;
     const long long T = (long long)p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
     const int entries = one ? (p.geom.pages + 1) / 2 : p.geom.pages;
     const int c0 = pd_holder(T, start, p.used), c1 = pd_holder(T, start + entries - 1, p.used);
-    const long long base = (long long)hk * sp_cols(p.geom) + col;
-    for (int c = c0; c <= c1; ++c)
-        for (int s = s0; s <= s1; ++s) {
-            const long long slot = 2 * (base + c) + s;
-            take(reinterpret_cast<const float2*>(p.part_ml)[slot * kSpRows + R % kSpRows],
-                 reinterpret_cast<const float4*>(p.part_o) +
-                     (slot * (D / 8) * kSpRows + u * kSpRows + R % kSpRows) * 2);
-        }
-    take(reinterpret_cast<const float2*>(p.own_ml)[row], reinterpret_cast<const float4*>(p.own_o + row * D) + 2 * u);
-    const int hq = hk * p.G + j / p.q_len, i = j % p.q_len;
+    const int parts = (c1 - c0 + 1) * (one ? 2 : 1);
+    const int64_t step = one ? 1 : 2;  // slots from a part to the next
+    const int64_t slot0 = 2 * ((int64_t)hk * sp_cols(p.geom) + col + c0) + s0;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot0 * kSpRows + r;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + (slot0 * (D / 4) + c4) * kSpRows + r;
+    wait_prerequisites();
+    const int64_t own = ((int64_t)b * p.Hkv + hk) * p.rows + j;
+    float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (takes) {
+        const float2 last = __ldcg(reinterpret_cast<const float2*>(p.own_ml) + own);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
+        M = last.x;
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[k * step * kSpRows].x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        auto take = [&](float2 w, float4 y) {
+            const float f = ex2_approx(w.x - Mu);
+            v[0] = fmaf(y.x, f, v[0]);
+            v[1] = fmaf(y.y, f, v[1]);
+            v[2] = fmaf(y.z, f, v[2]);
+            v[3] = fmaf(y.w, f, v[3]);
+            L = fmaf(w.y, f, L);
+        };
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) take(ml[k * step * kSpRows], __ldcg(po + k * step * (D / 4) * kSpRows));
+        take(last, x);
+    }
     const bool some = L > 0.f && M != -INFINITY;
     const float inv = some ? 1.f / L : L != L ? L : 0.f;
-    uint16_t* o = p.o + (int64_t)b * p.o_st0 + (int64_t)hq * p.o_st1 + (int64_t)i * p.o_st2 + 8 * u;
-    *reinterpret_cast<uint4*>(o) =
-        inv != 0.f ? make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
-                                pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv))
-                   : make_uint4(0u, 0u, 0u, 0u);
-    if (u == 0 && p.lse)
-        p.lse[((int64_t)b * p.Hkv * p.G + hq) * p.q_len + i] = some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+    out[lane][warp] = inv != 0.f ? make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv))
+                                 : make_uint2(0u, 0u);
+    if (warp == 0) {
+        where[lane] = takes ? (int64_t)b * p.o_st0 + (int64_t)hq * p.o_st1 + (int64_t)i * p.o_st2 : -1;
+        if (takes && p.lse && blockIdx.z == 0)
+            p.lse[((int64_t)b * p.Hkv * p.G + hq) * p.q_len + i] = some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+    }
+    __syncthreads();
+    const int row = threadIdx.x / kJoinWarps, u = threadIdx.x % kJoinWarps;
+    if (where[row] >= 0)
+        *reinterpret_cast<uint2*>(p.o + where[row] + blockIdx.z * kJoinCols + 4 * u) = out[row][u];
 }
 
 template <int D, int SCORE>
@@ -535,10 +591,9 @@ cudaError_t launch_shared_prefix(const SpParams& p, int D, int score_kind, cudaS
 
 cudaError_t launch_shared_join(const SpParams& p, int D, cudaStream_t stream)
 {
-    const long long threads = (long long)p.B * p.Hkv * p.rows * (D / 8);
-    const dim3 grid((unsigned)((threads + kJoinThreads - 1) / kJoinThreads));
-    return D == 64 ? launch_after(shared_join_kernel<64>, grid, kJoinThreads, 0, stream, p)
-                   : launch_after(shared_join_kernel<128>, grid, kJoinThreads, 0, stream, p);
+    const dim3 grid((unsigned)((p.geom.rows + 31) / 32), (unsigned)p.Hkv, (unsigned)(D / kJoinCols));
+    return D == 64 ? launch_after(shared_join_kernel<64>, grid, 32 * kJoinWarps, 0, stream, p)
+                   : launch_after(shared_join_kernel<128>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
 } // namespace fa

@@ -29,7 +29,7 @@ struct SpParams {
     int32_t used;    // CTAs, each with a share of the list
     // Partial results: of CTA c's piece of column col (counted over the heads) and stream
     // s, slot 2 (col + c) + s
-    float* part_o;   // [slot][D / 8][128][8] fp32, unnormalised
+    float* part_o;   // [slot][D / 4][128][4] fp32, unnormalised
     float* part_ml;  // [slot][128][2]: running max (log2 units), sum
 
     // join
