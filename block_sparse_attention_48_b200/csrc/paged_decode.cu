@@ -12,7 +12,9 @@
 // same number of bytes whatever the lengths are.  Each CTA finds its share by a scan
 // of the lengths.  K and V arrive by TMA in a ring; each of the eight compute warps
 // takes 16 keys of every page, the group's query rows being the n = 8 side of
-// m16n8k16 MMAs, with an online softmax of its own.  At the end of a piece of a
+// m16n8k16 MMAs, with an online softmax of its own.  (Two groups of warps on alternate
+// pages with 32 keys a warp need fewer instructions, but wait for one another at every
+// end of a segment: 16 ragged sequences 59 us, 53 like this.)  At the end of a piece of a
 // segment the warps' states are joined in shared memory.  A piece that is a whole
 // segment is written out at once; else its state goes to the workspace and the CTA
 // that completes the segment (a counter, which wraps back to zero) joins
@@ -43,15 +45,14 @@ constexpr int kBox = 16384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, int NR>
+template <int D>
 struct PdCfg {
     static constexpr int TILE = 128 * D * 2;       // K or V of one page and kv head
     static constexpr int NS = D == 128 ? 2 : 4;    // ring stages, 128 KB in flight per SM
     static constexpr int STAGE = 2 * TILE;
     static constexpr int OROW = D + 4;             // padded row of the joining buffer (bank spread)
-    static constexpr int OFF_JOIN = NS * STAGE;
-    static constexpr int SMEM = OFF_JOIN + kPdWarps * 8 * NR * OROW * 4 + 1024;
-    static_assert(SMEM <= 227 * 1024, "shared memory beyond 227 KB per CTA");
+    static constexpr int OFF_JOIN = NS * STAGE;    // eight rows of every warp at a time
+    static constexpr int SMEM = OFF_JOIN + kPdWarps * 8 * OROW * 4 + 1024;
 };
 
 struct __align__(16) PdShared {
@@ -60,8 +61,8 @@ struct __align__(16) PdShared {
     long long total;                        // list length
     int used;                               // CTAs that have work
     PdWalk start;                           // where this CTA's share starts
-    int last;                               // this CTA completed the segment
-    float m[kPdWarps][kPdMaxRows], l[kPdWarps][kPdMaxRows];
+    int last[2];                            // this CTA completed the split segment
+    float m[kPdWarps][8], l[kPdWarps][8];   // of eight rows
 };
 
 __device__ __forceinline__ void compute_sync()
@@ -128,11 +129,11 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
 template <int D, int SCORE, int NR>
 __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __grid_constant__ PdParams p)
 {
-    using C = PdCfg<D, NR>;
+    using C = PdCfg<D>;
     constexpr int KD = D / 16;
-    constexpr int RMAX = 8 * NR;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PdShared sh;
+    static_assert(C::SMEM + sizeof(sh) <= 227 * 1024, "shared memory beyond 227 KB per CTA");
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     bool bad = false;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     const int used = sh.used;
     const bool works = (int)blockIdx.x < used;
     const long long x0 = works ? pd_share(T, blockIdx.x, used) : 0;
-    const long long count = works ? pd_share(T, blockIdx.x + 1, used) - x0 : 0;
+    const int count = works ? (int)(pd_share(T, blockIdx.x + 1, used) - x0) : 0;
     PdWalk w{0, 0, 0, {0, 0, 0, 0}};
     if (works) w = sh.start;
 
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         uint32_t issued = 0;
         bool ok = true;
         int page_lane = 0, chunk = -1;
-        for (long long i = 0; i < count; ++i, ++issued) {
+        for (int i = 0; i < count; ++i, ++issued) {
             if (chunk != (w.t & ~31)) {
                 chunk = w.t & ~31;
                 const int tt = chunk + lane;
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     // ---- compute warps: S^T = K Q^T for the warp's 16 keys, O^T += V^T P^T.  Thread
     // (g, tq) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and query rows 2 tq,
     // 2 tq + 1 (+ 8 per row tile).
-    const int g = lane >> 2, tq = lane & 3;
+    const int g = lane >> 2, tq = lane & 3, m4 = lane >> 3;
+    const int key0 = 16 * warp;  // the warp's first key of a page
     int tok[NR][2];      // the token of each of the thread's rows
     bool rvalid[NR][2];
     int hq_g[NR][2];     // and its head within the group
@@ -276,12 +278,12 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             p.lse[((int64_t)b * p.Hq + hq) * p.q_len + i] = some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
     };
 
-    // The end of a piece: the warps' states joined, and the segment written out if
-    // this was its last piece to arrive.
-    auto end_piece = [&](const PdWalk& at, long long xseg) {
-        compute_sync();  // the last piece's states have been read
+    // The end of a piece: the warps' states joined, and written out if it is a whole
+    // segment, else left as a partial result.
+    auto end_piece = [&](const PdWalk& at, int c0, int c1) {
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
+        for (int nt = 0; nt < NR; ++nt) {
+            compute_sync();  // the buffer's last states have been read
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float l = l_run[nt][j];  // sum over the eight key groups
@@ -289,258 +291,327 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
                 if (g == 0) {
-                    sh.m[warp][8 * nt + 2 * tq + j] = m_run[nt][j];
-                    sh.l[warp][8 * nt + 2 * tq + j] = l;
+                    sh.m[warp][2 * tq + j] = m_run[nt][j];
+                    sh.l[warp][2 * tq + j] = l;
                 }
-                const int r = 8 * nt + 2 * tq + j;
-                float* dst = join + (warp * RMAX + r) * C::OROW + g;
+                float* dst = join + (warp * 8 + 2 * tq + j) * C::OROW + g;
 #pragma unroll
                 for (int mt = 0; mt < KD; ++mt) {
                     dst[16 * mt] = oacc[mt][nt][j];
                     dst[16 * mt + 8] = oacc[mt][nt][2 + j];
                 }
             }
-        compute_sync();
-        const int c0 = pd_holder(T, xseg, used), c1 = pd_holder(T, xseg + at.r.n - 1, used);
-        const int items = p.rows * (D / 4);
-        for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
-            const int r = it / (D / 4), d = (it % (D / 4)) * 4;
-            float M = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kPdWarps; ++k) M = fmaxf(M, sh.m[k][r]);
-            const float Mu = M == -INFINITY ? 0.f : M;
-            float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < kPdWarps; ++k) {
-                const float f = ex2_approx(sh.m[k][r] - Mu);
-                const float4 x = *reinterpret_cast<const float4*>(join + (k * RMAX + r) * C::OROW + d);
-                L = fmaf(sh.l[k][r], f, L);
-                v[0] = fmaf(x.x, f, v[0]);
-                v[1] = fmaf(x.y, f, v[1]);
-                v[2] = fmaf(x.z, f, v[2]);
-                v[3] = fmaf(x.w, f, v[3]);
-            }
-            if (c0 == c1) {
-                write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
-            } else {
-                const int64_t part = (2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x)) * p.rows + r;
-                __stcg(reinterpret_cast<float4*>(p.part_o + part * D + d), make_float4(v[0], v[1], v[2], v[3]));
-                if (d == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + part * 2), make_float2(M, L));
-            }
-        }
-        if (c0 != c1) {
-            __threadfence();
             compute_sync();
-            if (threadIdx.x == 0) {
-                const unsigned n = (unsigned)(c1 - c0);
-                sh.last = atomicInc(p.arrived + c0, n) == n;  // wraps to zero at the last piece
-                __threadfence();
-            }
-            compute_sync();
-            if (sh.last) {
-                __threadfence();
-                for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
-                    const int r = it / (D / 4), d = (it % (D / 4)) * 4;
-                    float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int c = c0; c <= c1; ++c) {
-                        const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows + r;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + part * 2));
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + part * D + d));
-                        const float Mn = fmaxf(M, ml.x), Mu = Mn == -INFINITY ? 0.f : Mn;
-                        const float a = ex2_approx(M - Mu), f = ex2_approx(ml.x - Mu);
-                        M = Mn;
-                        L = fmaf(ml.y, f, L * a);
-                        v[0] = fmaf(x.x, f, v[0] * a);
-                        v[1] = fmaf(x.y, f, v[1] * a);
-                        v[2] = fmaf(x.z, f, v[2] * a);
-                        v[3] = fmaf(x.w, f, v[3] * a);
-                    }
+            const int items = min(8, p.rows - 8 * nt) * (D / 4);
+            for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
+                const int r8 = it / (D / 4), r = 8 * nt + r8, d = (it % (D / 4)) * 4;
+                float M = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kPdWarps; ++k) M = fmaxf(M, sh.m[k][r8]);
+                const float Mu = M == -INFINITY ? 0.f : M;
+                float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < kPdWarps; ++k) {
+                    const float f = ex2_approx(sh.m[k][r8] - Mu);
+                    const float4 x = *reinterpret_cast<const float4*>(join + (k * 8 + r8) * C::OROW + d);
+                    L = fmaf(sh.l[k][r8], f, L);
+                    v[0] = fmaf(x.x, f, v[0]);
+                    v[1] = fmaf(x.y, f, v[1]);
+                    v[2] = fmaf(x.z, f, v[2]);
+                    v[3] = fmaf(x.w, f, v[3]);
+                }
+                if (c0 == c1) {
                     write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
+                } else {
+                    const int64_t part = (2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x)) * p.rows + r;
+                    __stcg(reinterpret_cast<float4*>(p.part_o + part * D + d), make_float4(v[0], v[1], v[2], v[3]));
+                    if (d == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + part * 2), make_float2(M, L));
                 }
             }
         }
     };
 
+    // The last piece of a split segment to arrive joins them all, in list order.  Only the
+    // first piece of a share (the end or the middle of a segment) and the last (the start
+    // of one) can be split; both arrive at the share's end, where the fence's and the
+    // counters' latency holds up nothing.
+    auto join_parts = [&](const PdWalk& at, int c0, int c1) {
+        for (int it = threadIdx.x; it < p.rows * (D / 4); it += 32 * kPdWarps) {
+            const int r = it / (D / 4), d = (it % (D / 4)) * 4;
+            const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + r;
+            const float* po = p.part_o + (int64_t)r * D + d;
+            float M = -INFINITY;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(ml + (2 * (int64_t)c + (c == c0)) * p.rows).x);
+            const float Mu = M == -INFINITY ? 0.f : M;
+            float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+                const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows;
+                const float2 w = __ldcg(ml + part);
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(po + part * D));
+                const float f = ex2_approx(w.x - Mu);
+                L = fmaf(w.y, f, L);
+                v[0] = fmaf(x.x, f, v[0]);
+                v[1] = fmaf(x.y, f, v[1]);
+                v[2] = fmaf(x.z, f, v[2]);
+                v[3] = fmaf(x.w, f, v[3]);
+            }
+            write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
+        }
+    };
+
     const float F = SCORE == FA_SCORE_SOFTCAP ? p.softcap * kLog2e : p.scale * kLog2e;
-    if (count > 0) load_segment(w.b, w.hk);
-    reset();
-    long long xseg = x0 - w.t;  // list position of the segment's first page
-    for (long long i = 0; i < count; ++i) {
-        PdWalk wn = w;
-        if (i + 1 < count) pd_advance(p, wn, bad);
-        const uint32_t slot = (uint32_t)(i % C::NS), use = (uint32_t)(i / C::NS);
-        // after a timeout the warp still walks its share (without computing), so that
-        // the pieces' barriers and counters stay whole
-        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[slot], use & 1, wd));
-        if (ok) {
-            const uint32_t kbase = smem_u32(smem + slot * C::STAGE), vbase = kbase + C::TILE;
-            const int key0 = 16 * warp;
-            const int m4 = lane >> 3;
-            const int kv0 = (w.r.lo + w.t) * 128;
-            const int pos0 = w.r.len - p.q_len, pos1 = w.r.len - 1;  // first and last query row's positions
-            // some row does not attend the whole page
-            const bool edge = kv0 + 127 > pos0 || (p.has_window && kv0 < pos1 - p.window);
-
-            constexpr bool kEarly = !(D == 128 && NR == 2);
-            uint32_t ka[kEarly ? KD : 1][4], va[kEarly ? KD : 1][4];
-            if constexpr (kEarly) {
+    // One page: the warp's 16 keys, the first of them kv0.  kEarly: all of their K and V is
+    // taken to registers first and the ring's slot given back before the products.
+    constexpr bool kEarly = !(D == 128 && NR == 2);
+    auto page = [&](uint32_t kbase, uint32_t vbase, int kv0, int pos0, int pos1, bool edge, uint64_t* freed) {
+        uint32_t ka[kEarly ? KD : 1][4], va[kEarly ? KD : 1][4];
+        if constexpr (kEarly) {
 #pragma unroll
-                for (int kk = 0; kk < KD; ++kk)
-                    ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[kk]);
-#pragma unroll
-                for (int mt = 0; mt < KD; ++mt)
-                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[mt]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.empty[slot]);
-            }
-            float sacc[NR][4];
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KD; ++kk) {
-                if constexpr (!kEarly)
-                    ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[0]);
-#pragma unroll
-                for (int nt = 0; nt < NR; ++nt)
-                    mma_bf16_16816(sacc[nt], ka[kEarly ? kk : 0], qb[nt][kk][0], qb[nt][kk][1]);
-            }
-
-            // score_mod in log2 units; masked scores are replaced
-            float mt_[NR][2];
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) mt_[nt][j] = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e & 1;
-                    const int kv = kv0 + key0 + g + 8 * (e >> 1);
-                    const int pos = pos0 + tok[nt][j];
-                    bool adm = rvalid[nt][j];
-                    if (edge) adm = adm && kv <= pos && (!p.has_window || (int64_t)pos - kv <= p.window);
-                    float x = sacc[nt][e];
-                    if constexpr (SCORE == FA_SCORE_SOFTCAP) x = tanh_accurate(x * p.softcap_in) * F;
-                    else if constexpr (SCORE == FA_SCORE_ALIBI) x = fmaf(slope[nt][j], (float)(kv - pos), x * F);
-                    else x = x * F;
-                    x = adm ? x : -INFINITY;
-                    sacc[nt][e] = x;
-                    mt_[nt][j] = fmaxf(mt_[nt][j], x);
-                }
-            float alpha[NR][2], m_use[NR][2];
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = mt_[nt][j];
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                    const float m_new = fmaxf(m_run[nt][j], m);
-                    m_use[nt][j] = m_new == -INFINITY ? 0.f : m_new;
-                    alpha[nt][j] = ex2_approx(m_run[nt][j] - m_use[nt][j]);  // 0 while nothing was admitted
-                    m_run[nt][j] = m_new;
-                    l_run[nt][j] *= alpha[nt][j];
-                }
-            // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor core's operand
-            // type); the sum is taken of the unrounded values
-            uint32_t pb[NR][2];
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt) {
-                float pv[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    pv[e] = ex2_approx(sacc[nt][e] - m_use[nt][e & 1]);
-                    l_run[nt][e & 1] += pv[e];
-                }
-                pb[nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
-                pb[nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
-            }
+            for (int kk = 0; kk < KD; ++kk)
+                ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[kk]);
 #pragma unroll
             for (int mt = 0; mt < KD; ++mt)
+                ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[mt]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(freed);
+        }
+        float sacc[NR][4], sodd[NR][4];  // two chains of products
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[nt][e] = sodd[nt][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) {
+            if constexpr (!kEarly)
+                ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[0]);
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+                mma_bf16_16816(kk & 1 ? sodd[nt] : sacc[nt], ka[kEarly ? kk : 0], qb[nt][kk][0], qb[nt][kk][1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[nt][e] += sodd[nt][e];
+        if constexpr (SCORE == FA_SCORE_SOFTCAP) {
+            // tanh: the polynomial, and the far form where the warp has a far score
+            bool far = false;
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sacc[nt][e] *= p.softcap_in;
+                    far |= fabsf(sacc[nt][e]) > kTanhPolyMax;
+                }
+            const bool any = __any_sync(0xFFFFFFFFu, far);
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float y0 = sacc[nt][e], y1 = sacc[nt][e + 1];
+                    float t0, t1;
+                    f2_unpack(tanh_poly2(f2_pack(y0, y1)), t0, t1);
+                    if (any) {
+                        const float u0 = tanh_far(y0), u1 = tanh_far(y1);
+                        t0 = fabsf(y0) > kTanhPolyMax ? u0 : t0;
+                        t1 = fabsf(y1) > kTanhPolyMax ? u1 : t1;
+                    }
+                    sacc[nt][e] = t0;
+                    sacc[nt][e + 1] = t1;
+                }
+        }
+
+        // score_mod in log2 units; masked scores are replaced
+        float mt_[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mt_[nt][j] = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = e & 1;
+                const int kv = kv0 + g + 8 * (e >> 1);
+                const int pos = pos0 + tok[nt][j];
+                bool adm = rvalid[nt][j];
+                if (edge) adm = adm && kv <= pos && (!p.has_window || (int64_t)pos - kv <= p.window);
+                float x = sacc[nt][e];
+                if constexpr (SCORE == FA_SCORE_SOFTCAP) x = x * F;  // capped above
+                else if constexpr (SCORE == FA_SCORE_ALIBI) x = fmaf(slope[nt][j], (float)(kv - pos), x * F);
+                else x = x * F;
+                x = adm ? x : -INFINITY;
+                sacc[nt][e] = x;
+                mt_[nt][j] = fmaxf(mt_[nt][j], x);
+            }
+        float alpha[NR][2], m_use[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float m = mt_[nt][j];
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                const float m_new = fmaxf(m_run[nt][j], m);
+                m_use[nt][j] = m_new == -INFINITY ? 0.f : m_new;
+                alpha[nt][j] = ex2_approx(m_run[nt][j] - m_use[nt][j]);  // 0 while nothing was admitted
+                m_run[nt][j] = m_new;
+                l_run[nt][j] *= alpha[nt][j];
+            }
+        // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor core's operand
+        // type); the sum is taken of the unrounded values
+        uint32_t pb[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+            float pv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pv[e] = ex2_approx(sacc[nt][e] - m_use[nt][e & 1]);
+                l_run[nt][e & 1] += pv[e];
+            }
+            pb[nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
+            pb[nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
+        }
+#pragma unroll
+        for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
+        if (!edge) {
+#pragma unroll
+            for (int mt = 0; mt < KD; ++mt) {
+                if constexpr (!kEarly)
+                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[0]);
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
+                    mma_bf16_16816(oacc[mt][nt], va[kEarly ? mt : 0], pb[nt][0], pb[nt][1]);
+            }
+        } else {
+            // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the
+            // same + 8 that a row at positions [from, to] may attend
+            auto keep = [&](int from, int to, uint32_t (&k2)[2]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
-            if (!edge) {
-#pragma unroll
-                for (int mt = 0; mt < KD; ++mt) {
-                    if constexpr (!kEarly)
-                        ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[0]);
-#pragma unroll
-                    for (int nt = 0; nt < NR; ++nt)
-                        mma_bf16_16816(oacc[mt][nt], va[kEarly ? mt : 0], pb[nt][0], pb[nt][1]);
+                for (int h = 0; h < 2; ++h) {
+                    const int kv = kv0 + 2 * tq + 8 * h;
+                    const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
+                    const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
+                    k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
                 }
-            } else {
-                // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the
-                // same + 8 that a row at positions [from, to] may attend
-                auto keep = [&](int from, int to, uint32_t (&k2)[2]) {
+            };
+            uint32_t any2[2];
+            keep(pos0, pos1, any2);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int kv = kv0 + key0 + 2 * tq + 8 * h;
-                        const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
-                        const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
-                        k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
-                    }
-                };
-                uint32_t any2[2];
-                keep(pos0, pos1, any2);
+            for (int mt = 0; mt < KD; ++mt) {
+                uint32_t vr[4];
+                if constexpr (!kEarly) {
+                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), vr);
+                } else {
 #pragma unroll
-                for (int mt = 0; mt < KD; ++mt) {
-                    uint32_t vr[4];
-                    if constexpr (!kEarly) {
-                        ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), vr);
-                    } else {
+                    for (int e = 0; e < 4; ++e) vr[e] = va[mt][e];
+                }
+                bool odd = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) vr[e] = va[mt][e];
-                    }
-                    bool odd = false;
+                for (int e = 0; e < 4; ++e) {
+                    vr[e] &= any2[e >> 1];
+                    odd |= nonfinite2(vr[e]);
+                }
+                if (p.q_len > 1 && __any_sync(0xFFFFFFFFu, odd)) {
+                    // an infinity or NaN that some rows attend and others may not: one
+                    // product per token, each with its own keys, kept for its rows only
+                    for (int i = 0; i < p.q_len; ++i) {
+                        uint32_t k2[2], vi[4];
+                        keep(pos0 + i, pos0 + i, k2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        vr[e] &= any2[e >> 1];
-                        odd |= nonfinite2(vr[e]);
-                    }
-                    if (p.q_len > 1 && __any_sync(0xFFFFFFFFu, odd)) {
-                        // an infinity or NaN that some rows attend and others may not: one
-                        // product per token, each with its own keys, kept for its rows only
-                        for (int i = 0; i < p.q_len; ++i) {
-                            uint32_t k2[2], vi[4];
-                            keep(pos0 + i, pos0 + i, k2);
+                        for (int e = 0; e < 4; ++e) vi[e] = vr[e] & k2[e >> 1];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) vi[e] = vr[e] & k2[e >> 1];
+                        for (int nt = 0; nt < NR; ++nt) {
+                            float d4[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_bf16_16816(d4, vi, pb[nt][0], pb[nt][1]);
 #pragma unroll
-                            for (int nt = 0; nt < NR; ++nt) {
-                                float d4[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_bf16_16816(d4, vi, pb[nt][0], pb[nt][1]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (tok[nt][e & 1] == i) oacc[mt][nt][e] += d4[e];
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                if (tok[nt][e & 1] == i) oacc[mt][nt][e] += d4[e];
                         }
-                    } else {
-#pragma unroll
-                        for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(oacc[mt][nt], vr, pb[nt][0], pb[nt][1]);
                     }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(oacc[mt][nt], vr, pb[nt][0], pb[nt][1]);
                 }
             }
-            if constexpr (!kEarly) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        }
+    };
+
+    // the share's first and last piece where they are parts of a split segment
+    PdWalk head = w, tail = w;
+    int head0 = -1, head1 = -1, tail0 = -1, tail1 = -1;
+    if (count > 0) load_segment(w.b, w.hk);
+    long long xseg = x0 - w.t;  // list position of the segment's first page
+    uint32_t slot = 0, phase = 0;
+    for (int done = 0; done < count;) {
+        // a piece: pages [w.t, w.t + n) of the segment
+        const int n = min(w.r.n - w.t, count - done);
+        const int pos0 = w.r.len - p.q_len, pos1 = w.r.len - 1;  // first and last query row's positions
+        int kv0 = (w.r.lo + w.t) * 128 + key0;                   // the warp's first key
+        reset();
+        for (int i = 0; i < n; ++i, kv0 += 128) {
+            // after a timeout the warp still walks its share (without computing), so that
+            // the pieces' barriers and counters stay whole
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[slot], phase, wd))) {
+                const uint32_t kbase = smem_u32(smem + slot * C::STAGE), vbase = kbase + C::TILE;
+                // no row attends any of the warp's keys, or some row not all of them
+                const bool none = kv0 > pos1 || (p.has_window && kv0 + 15 < pos0 - p.window);
+                const bool edge = kv0 + 15 > pos0 || (p.has_window && kv0 < pos1 - p.window);
+                if (!none) page(kbase, vbase, kv0, pos0, pos1, edge, &sh.empty[slot]);
+                if (none || !kEarly) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                }
+            }
+            if (++slot == C::NS) {
+                slot = 0;
+                phase ^= 1;
             }
         }
-        // the piece ends with the segment or with the share
-        if (i + 1 == count || wn.t == 0) {
-            if (i + 1 < count) load_segment(wn.b, wn.hk);  // its latency passes during the join
-            end_piece(w, xseg);
-            if (i + 1 < count) {
-                xseg += w.r.n;
-                reset();
+        done += n;
+        const int c0 = pd_holder(T, xseg, used), c1 = pd_holder(T, xseg + w.r.n - 1, used);
+        PdWalk next = w;
+        next.t += n - 1;
+        if (done < count) {
+            pd_advance(p, next, bad);
+            load_segment(next.b, next.hk);  // its latency passes during the join
+        }
+        end_piece(w, c0, c1);
+        if (c0 != c1) {
+            if (xseg < x0) {
+                head = w;
+                head0 = c0;
+                head1 = c1;
+            } else {
+                tail = w;
+                tail0 = c0;
+                tail1 = c1;
             }
         }
-        w = wn;
+        xseg += w.r.n;
+        w = next;
+    }
+    if (head0 >= 0 || tail0 >= 0) {
+        compute_sync();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            const unsigned nh = (unsigned)(head1 - head0), nt = (unsigned)(tail1 - tail0);
+            unsigned h = 0, t = 0;  // the counters wrap to zero at the last piece
+            if (head0 >= 0) h = atomicInc(p.arrived + head0, nh);
+            if (tail0 >= 0) t = atomicInc(p.arrived + tail0, nt);
+            sh.last[0] = head0 >= 0 && h == nh;
+            sh.last[1] = tail0 >= 0 && t == nt;
+            __threadfence();
+        }
+        compute_sync();
+        if (sh.last[0]) join_parts(head, head0, head1);
+        if (sh.last[1]) join_parts(tail, tail0, tail1);
     }
     // sequences without a key: O = 0, LSE = -inf
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -574,14 +645,14 @@ cudaError_t launch_variant(const PdParams& p, cudaStream_t stream)
             for (const CtxKey& k : done) have |= k == key;
         if (!have) {
             cudaError_t e =
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<D, NR>::SMEM);
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<D>::SMEM);
             if (e != cudaSuccess) return e;
             if (current_ctx(&key)) done.push_back(key);
         }
     }
     if (p.prefix_pages > 0)  // beside the prefix's last CTAs
-        return launch_after(kern, dim3((unsigned)p.grid), kPdThreads, PdCfg<D, NR>::SMEM, stream, p);
-    kern<<<(unsigned)p.grid, kPdThreads, PdCfg<D, NR>::SMEM, stream>>>(p);
+        return launch_after(kern, dim3((unsigned)p.grid), kPdThreads, PdCfg<D>::SMEM, stream, p);
+    kern<<<(unsigned)p.grid, kPdThreads, PdCfg<D>::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 

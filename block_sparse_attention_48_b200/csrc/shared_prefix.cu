@@ -158,13 +158,15 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
     auto ready = [&](uint64_t* bar, uint32_t parity) {
         return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, wd));
     };
-    // A slot is free after two arrivals: one of each stream, or both of the one that reads it
-    auto release = [&](uint32_t slot, bool one) {
-        umma_commit(&sh.empty[slot]);
-        if (one) umma_commit(&sh.empty[slot]);
+    // A slot is free after an arrival of each stream.  In a column of one tile a stream
+    // passes over the other's tiles: it waits for them too, since a barrier's parity tells
+    // only its last phase and none may be skipped.
+    auto pass = [&](uint32_t pos) {
+        if (ready(&sh.full[pos % C::NS], (pos / C::NS) & 1) && elect_one_sync()) mbar_arrive(&sh.empty[pos % C::NS]);
+        __syncwarp();
     };
     // S of one half of a tile whose K has landed
-    auto scores = [&](uint32_t kpos, int h, bool one) {
+    auto scores = [&](uint32_t kpos, int h) {
         const uint32_t slot = kpos % C::NS, kd = k0 + slot * (uint32_t)(C::TILE >> 4) + h * kHalf;
         tc_fence_after();
         if (elect_one_sync()) {
@@ -175,12 +177,12 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
                 umma_ss(tmem + C::s_col(s, h), desc64(hi_k, qd + off), desc64(hi_k, kd + off), idesc_s, k > 0);
             }
             umma_commit(&sh.s_full[s][h]);
-            if (h == 1) release(slot, one);
+            if (h == 1) umma_commit(&sh.empty[slot]);
         }
         __syncwarp();
     };
     // O += P V of one half
-    auto values = [&](uint32_t vpos, int h, bool one, uint32_t accumulate) {
+    auto values = [&](uint32_t vpos, int h, uint32_t accumulate) {
         const uint32_t slot = vpos % C::NS, vd = v0 + slot * (uint32_t)(C::TILE >> 4) + h * kHalf;
         tc_fence_after();
         if (elect_one_sync()) {
@@ -189,7 +191,7 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
                 umma_ts(tmem + C::o_col(s), tmem + C::s_col(s, h) + 8 * k, desc64(hi_mn, vd + (uint32_t)(k * 128)),
                         idesc_o, k > 0 ? 1u : accumulate);
             umma_commit(&sh.pv_done[s]);
-            if (h == 1) release(slot, one);
+            if (h == 1) umma_commit(&sh.empty[slot]);
         }
         __syncwarp();
     };
@@ -199,27 +201,36 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
         if (n > 0) {
             SpSeq cur = entry_seq(p.geom, pc, pc.e0, s, at);
             if (ready(&sh.q_full[s], piece & 1) && ready(&sh.full[cur.k % C::NS], (cur.k / C::NS) & 1)) {
-                scores(cur.k, 0, pc.one);
-                scores(cur.k, 1, pc.one);
+                scores(cur.k, 0);
+                scores(cur.k, 1);
             }
             for (int i = 0; ok && i < n; ++i, ++tile) {
-                at += entry_tiles(p.geom, pc, pc.e0 + i);
+                const uint32_t tiles = entry_tiles(p.geom, pc, pc.e0 + i);
+                const bool both = pc.one && tiles == 4;  // the other stream has a tile of this entry
+                // its K before the next K is waited for, which may go to that slot
+                if (both) pass(at + 1 - s);
+                at += tiles;
                 const SpSeq nx = entry_seq(p.geom, pc, pc.e0 + i + 1, s, at);
                 const bool more = i + 1 < n;
                 ready(&sh.full[cur.v % C::NS], (cur.v / C::NS) & 1);
                 if (!ready(&sh.p_full[s][0], tile & 1)) break;
                 if (i == 0 && piece > 0 && !ready(&sh.o_empty[s], (piece - 1) & 1)) break;
-                values(cur.v, 0, pc.one, i > 0 ? 1u : 0u);
+                values(cur.v, 0, i > 0 ? 1u : 0u);
                 if (more && !ready(&sh.full[nx.k % C::NS], (nx.k / C::NS) & 1)) break;
-                if (more) scores(nx.k, 0, pc.one);
+                if (more) scores(nx.k, 0);
                 if (!ready(&sh.p_full[s][1], tile & 1)) break;
-                values(cur.v, 1, pc.one, 1u);
-                if (more) scores(nx.k, 1, pc.one);
+                values(cur.v, 1, 1u);
+                if (more) scores(nx.k, 1);
+                if (both) pass(at - 1 - s);
                 cur = nx;
             }
             ++piece;
         }
-        for (int i = n; i < pc.n; ++i) at += entry_tiles(p.geom, pc, pc.e0 + i);
+        if (ok && n < pc.n) {  // the last entry is the other stream's alone
+            pass(at);
+            pass(at + 1);
+            at += 2;
+        }
         x += pc.n;
     }
     // the products in flight end before tensor memory is given back (bounded)
@@ -415,8 +426,10 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
             }
         }
         if (!ok) break;
-        // the piece's last P V (and so all its products)
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 1) & 1, wd));
+        // the piece's last two P V (and so all its products), one phase after the other: of
+        // an earlier one than the next a parity tells nothing
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 2) & 1, wd)) &&
+             __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 1) & 1, wd));
         if (!ok) break;
         ++piece;
         tc_fence_after();

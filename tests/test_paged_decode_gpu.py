@@ -124,6 +124,27 @@ def test_decode_paged_far_pages():
     assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
 
 
+@pytest.mark.parametrize("shape", [(8, 8, 128, 1), (8, 8, 64, 2), (32, 8, 128, 4)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_decode_with_many_pages_a_cta(shape, shared):
+    """Shares of 20 and more pages a CTA that run over several segments, and an odd number
+    of shared pages: the rings of tiles go round many times; calls one after another give
+    the same bits."""
+    fa = _fa()
+    Hq, Hkv, D, n = shape
+    prefix = 301 * PAGE if shared else 0
+    lens = [prefix + 11000, prefix + 300] if shared else [47003, 2, 5100]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=77, prefix=prefix, filler=float("nan"))
+    args = [t.cuda() for t in (q, k, v, table, sl)]
+    call = (lambda: fa.flex_decode_shared(*args, prefix)) if shared else (lambda: fa.flex_decode_paged(*args))
+    got = call()
+    assert_decode(got, decode_ref(q, k, v, table, lens))
+    for _ in range(20):
+        again = call()
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
+
+
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length"])
 def test_decode_paged_reports_bad_tables_and_lengths(what, shared):
