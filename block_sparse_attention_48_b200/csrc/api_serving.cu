@@ -209,23 +209,23 @@ int fa_paged_append(const fa_tensor* k, const fa_tensor* v, const fa_tensor* q, 
 
 namespace {
 
-// Workspace of a paged decode: the status word, a counter per CTA, then per partial
-// result (two per CTA) the (running max, sum) and the unnormalised O of every packed
+// Workspace of a paged decode: the status word, a counter per team, then per partial
+// result (two per team) the (running max, sum) and the unnormalised O of every packed
 // query row, each part 256-byte aligned.  The counters lie at the same place for every
 // shape, since they alone must be zero when a call starts.  With a shared prefix, the
 // prefix's partial results and every row's own state follow.
 struct PdLayout {
     size_t arrived, ml, o, pre_ml, pre_o, own_ml, own_o, end;
-    int sms, pre_ctas;  // one CTA per SM; CTAs of the prefix
+    int sms, pre_ctas;  // CTAs of a paged decode at most, CTAs of the prefix
 };
 
 PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
 {
     PdLayout L;
     L.sms = sm_count();
-    const size_t ctas = L.sms > 0 ? L.sms : 1, parts = 2 * ctas * (size_t)rows;
+    const size_t ctas = L.sms > 0 ? L.sms : 1, teams = ctas * fa::kPdTeams, parts = 2 * teams * (size_t)rows;
     L.arrived = kWorkspaceBytes;
-    L.ml = L.arrived + align256(ctas * sizeof(uint32_t));
+    L.ml = L.arrived + align256(teams * sizeof(uint32_t));
     L.o = L.ml + align256(parts * 2 * sizeof(float));
     L.end = L.o + parts * D * sizeof(float);
     L.pre_ml = L.pre_o = L.own_ml = L.own_o = 0;
@@ -307,8 +307,9 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
         P.softcap_in = P.scale / sm->softcap;
     }
     P.slopes = kind == FA_SCORE_ALIBI ? sm->alibi_slopes : nullptr;
-    const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more than pages in all
+    const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more teams than pages in all
     P.grid = (int32_t)(most < 1 ? 1 : most < lay.sms ? most : lay.sms);
+    P.teams = (int32_t)(most < 1 ? 1 : most < P.grid * fa::kPdTeams ? most : P.grid * fa::kPdTeams);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     P.part_ml = reinterpret_cast<float*>(ws + lay.ml);

@@ -7,15 +7,15 @@
 //   at or before it (and within the window);  out = softmax(mod(q k^T scale)) v
 //
 // Bound: HBM (K and V of the pages are read once; 4 G flops per byte of them).
-// Work split: the pages of all (sequence, kv head) segments form one list, and CTA c
-// of a grid of one CTA per SM takes its c-th equal share, so every SM streams the
-// same number of bytes whatever the lengths are.  Each CTA finds its share by a scan
-// of the lengths.  K and V arrive by TMA in a ring; each of the eight compute warps
-// takes 16 keys of every page, the group's query rows being the n = 8 side of
-// m16n8k16 MMAs, with an online softmax of its own.  (Two groups of warps on alternate
-// pages with 32 keys a warp need fewer instructions, but wait for one another at every
-// end of a segment: 16 ragged sequences 59 us, 53 like this.)  At the end of a piece of a
-// segment the warps' states are joined in shared memory.  A piece that is a whole
+// Work split: the pages of all (sequence, kv head) segments form one list, and team c of
+// two teams per SM takes its c-th equal share, so every SM streams the same number of
+// bytes whatever the lengths are.  Each CTA finds its teams' shares by a scan of the
+// lengths.  A team is a TMA producer warp, a ring of K and V tiles and four compute
+// warps that take 32 keys of every page each, the query rows being the n = 8 side of
+// m16n8k16 MMAs, with an online softmax of each warp's own.  The teams have nothing to
+// wait for in one another: while one ends a segment or waits for a page, the other
+// computes.  At the end of a piece of a segment a team's states are joined in shared
+// memory.  A piece that is a whole
 // segment is written out at once; else its state goes to the workspace and the CTA
 // that completes the segment (a counter, which wraps back to zero) joins
 // the pieces in list order, so that results do not depend on who comes last.
@@ -48,26 +48,28 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D>
 struct PdCfg {
     static constexpr int TILE = 128 * D * 2;       // K or V of one page and kv head
-    static constexpr int NS = D == 128 ? 2 : 4;    // ring stages, 128 KB in flight per SM
-    static constexpr int STAGE = 2 * TILE;
+    static constexpr int NT = D == 128 ? 3 : 6;    // tiles of a team's ring, 96 KB
     static constexpr int OROW = D + 4;             // padded row of the joining buffer (bank spread)
-    static constexpr int OFF_JOIN = NS * STAGE;    // eight rows of every warp at a time
-    static constexpr int SMEM = OFF_JOIN + kPdWarps * 8 * OROW * 4 + 1024;
+    static constexpr int JOIN = kPdWarps * 8 * OROW * 4;  // eight rows of every warp at a time
+    static constexpr int OFF_JOIN = kPdTeams * NT * TILE;
+    static constexpr int SMEM = OFF_JOIN + kPdTeams * JOIN + 1024;
 };
 
 struct __align__(16) PdShared {
-    uint64_t full[4], empty[4];
+    uint64_t full[kPdTeams][6], empty[kPdTeams][6];
     long long scan[kPdThreads / 32];
-    long long total;                        // list length
-    int used;                               // CTAs that have work
-    PdWalk start;                           // where this CTA's share starts
-    int last[2];                            // this CTA completed the split segment
-    float m[kPdWarps][8], l[kPdWarps][8];   // of eight rows
+    long long total;                          // list length
+    int used;                                 // teams that have work
+    PdWalk start[kPdTeams];                   // where a team's share starts
+    int last[kPdTeams][2];                    // this team completed the split segment
+    uint16_t row_at[kPdMaxRows];              // a query row's head in its group * 256 + its token
+    float m[kPdTeams][kPdWarps][8], l[kPdTeams][kPdWarps][8];  // of eight rows
 };
 
-__device__ __forceinline__ void compute_sync()
+// The compute warps of a team.
+__device__ __forceinline__ void team_sync(int team)
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kPdWarps) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kPdWarps) : "memory");
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x)
@@ -90,7 +92,11 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w)
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-// All threads: the list's length and where this CTA's share starts.
+// Team of the work split: the first teams of all CTAs come before the second ones, so
+// that a short list is spread over the SMs.
+__device__ __forceinline__ int pd_team(int team) { return (int)blockIdx.x + (int)gridDim.x * team; }
+
+// All threads: the list's length and where this CTA's shares start.
 __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool& bad)
 {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -112,16 +118,17 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
         total += sh.scan[w];
     }
     const long long T = total * p.Hkv;
-    const int used = (int)min(T, (long long)p.grid);
+    const int used = (int)min(T, (long long)p.teams);
     if (tid == 0) {
         sh.total = T;
         sh.used = used;
     }
-    if ((int)blockIdx.x < used) {
-        const long long x0 = pd_share(T, blockIdx.x, used);
-        long long acc = before + inc - mine;  // pages of the sequences before this thread's
-        if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + mine))
-            pd_find(p, x0, lo, hi, acc, sh.start, bad);
+#pragma unroll
+    for (int team = 0; team < kPdTeams; ++team) {
+        if (pd_team(team) >= used) continue;
+        const long long x0 = pd_share(T, pd_team(team), used);
+        const long long acc = before + inc - mine;  // pages of the sequences before this thread's
+        if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + mine)) pd_find(p, x0, lo, hi, acc, sh.start[team], bad);
     }
     __syncthreads();
 }
@@ -141,47 +148,56 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     launch_dependents();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], kPdWarps);
-        }
+        for (int t = 0; t < kPdTeams; ++t)
+            for (int i = 0; i < C::NT; ++i) {
+                mbar_init(&sh.full[t][i], 1);
+                mbar_init(&sh.empty[t][i], kPdWarps);
+            }
         mbar_fence_init();
     }
+    if (threadIdx.x < p.rows)
+        sh.row_at[threadIdx.x] = (uint16_t)(threadIdx.x / p.q_len * 256 + threadIdx.x % p.q_len);
     pd_locate(p, sh, bad);  // ends with a CTA barrier
+    const int team = warp < kPdTeams * kPdWarps ? warp / kPdWarps : warp - kPdTeams * kPdWarps;
+    const int me = pd_team(team);
+    uint64_t *full = sh.full[team], *empty = sh.empty[team];
+    uint8_t* ring = smem + team * C::NT * C::TILE;
     const long long T = sh.total;
     const int used = sh.used;
-    const bool works = (int)blockIdx.x < used;
-    const long long x0 = works ? pd_share(T, blockIdx.x, used) : 0;
-    const int count = works ? (int)(pd_share(T, blockIdx.x + 1, used) - x0) : 0;
+    const bool works = me < used;
+    const long long x0 = works ? pd_share(T, me, used) : 0;
+    const int count = works ? (int)(pd_share(T, me + 1, used) - x0) : 0;
     PdWalk w{0, 0, 0, {0, 0, 0, 0}};
-    if (works) w = sh.start;
+    if (works) w = sh.start[team];
 
-    if (warp == kPdWarps) {
-        // TMA producer: K and V of every page of the share.  Lane i holds the page of
-        // the (t & ~31) + i-th page of the segment's range.
-        uint32_t issued = 0;
+    if (warp >= kPdTeams * kPdWarps) {
+        // TMA producer: K and V of every page of the share.  Lane l holds the page of the
+        // (t & ~31) + l-th page of the segment's range.
+        uint32_t issued = 0;  // tiles
         bool ok = true;
         int page_lane = 0, chunk = -1;
-        for (int i = 0; i < count; ++i, ++issued) {
+        auto load = [&](const CUtensorMap* tm, int hk, int page) {
+            const uint32_t slot = issued % C::NT, use = issued / C::NT;
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], (use & 1) ^ 1, wd));
+            if (!ok) return;
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(&full[slot], C::TILE);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(ring + slot * C::TILE + c * kBox, tm, &full[slot], c * 64, 0, hk, page);
+            }
+            __syncwarp();
+            ++issued;
+        };
+        for (int i = 0; ok && i < count; ++i) {
             if (chunk != (w.t & ~31)) {
                 chunk = w.t & ~31;
                 const int tt = chunk + lane;
                 page_lane = tt < w.r.n ? __ldg(p.page_table + (int64_t)w.b * p.pt_stride + w.r.lo + tt) : 0;
             }
             const int page = pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, w.t & 31), p.num_pages, bad);
-            const uint32_t slot = issued % C::NS, use = issued / C::NS;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.empty[slot], (use & 1) ^ 1, wd));
-            if (!ok) break;
-            if (elect_one_sync()) {
-                uint8_t* dst = smem + slot * C::STAGE;
-                mbar_arrive_expect_tx(&sh.full[slot], C::STAGE);
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    tma_load_4d(dst + c * kBox, &p.tm_k, &sh.full[slot], c * 64, 0, w.hk, page);
-                    tma_load_4d(dst + C::TILE + c * kBox, &p.tm_v, &sh.full[slot], c * 64, 0, w.hk, page);
-                }
-            }
-            __syncwarp();
+            load(&p.tm_k, w.hk, page);
+            load(&p.tm_v, w.hk, page);
             if (i + 1 < count) {
                 const int b = w.b;
                 pd_advance(p, w, bad);
@@ -190,10 +206,10 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
         // copies in flight land before the CTA exits (bounded)
         Watchdog dw{wd.failed ? 1000000ull : wd.limit_ns, false};
-        for (uint32_t j = 0; j < (uint32_t)C::NS && j < issued; ++j) {
+        for (uint32_t j = 0; j < (uint32_t)C::NT && j < issued; ++j) {
             const uint32_t last = issued - 1 - j;
             dw.failed = false;
-            mbar_wait(&sh.full[last % C::NS], (last / C::NS) & 1, dw);
+            mbar_wait(&full[last % C::NT], (last / C::NT) & 1, dw);
         }
         if (lane == 0 && (wd.failed || !ok)) atomicOr(p.status, STATUS_TIMEOUT);
         if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
@@ -201,11 +217,12 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         return;
     }
 
-    // ---- compute warps: S^T = K Q^T for the warp's 16 keys, O^T += V^T P^T.  Thread
-    // (g, tq) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and query rows 2 tq,
-    // 2 tq + 1 (+ 8 per row tile).
+    // ---- compute warps: S^T = K Q^T for two tiles of 16 keys, O^T += V^T P^T.  Thread
+    // (g, tq) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 of a tile and query rows
+    // 2 tq, 2 tq + 1 (+ 8 per row tile).
+    const int tid = threadIdx.x % (32 * kPdWarps), tw = warp % kPdWarps;  // within the team
     const int g = lane >> 2, tq = lane & 3, m4 = lane >> 3;
-    const int key0 = 16 * warp;  // the warp's first key of a page
+    const int key0 = 32 * tw;  // the warp's first key of a page
     int tok[NR][2];      // the token of each of the thread's rows
     bool rvalid[NR][2];
     int hq_g[NR][2];     // and its head within the group
@@ -220,21 +237,26 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         }
     float slope[NR][2];
     uint32_t qb[NR][KD][2];
+    int64_t q_off[NR];  // the B fragment's column: a query row's place in a sequence's and head's Q
+    bool q_in[NR];
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+        const int r = 8 * nt + g;
+        q_in[nt] = r < p.rows;
+        q_off[nt] = q_in[nt] ? (int64_t)(r / p.q_len) * p.q_st1 + (int64_t)(r % p.q_len) * p.q_st2 + 2 * tq : 0;
+    }
     auto load_segment = [&](int b, int hk) {
+        const uint16_t* seg = p.q + (int64_t)b * p.q_st0 + (int64_t)(hk * p.G) * p.q_st1;
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 slope[nt][j] = SCORE == FA_SCORE_ALIBI ? __ldg(p.slopes + hk * p.G + hq_g[nt][j]) * kLog2e : 0.f;
-            const int rb = 8 * nt + g;  // the B fragment's column
-            const bool vb = rb < p.rows;
-            const int rv = vb ? rb : 0;
-            const uint16_t* src = p.q + (int64_t)b * p.q_st0 + (int64_t)(hk * p.G + rv / p.q_len) * p.q_st1 +
-                                  (int64_t)(rv % p.q_len) * p.q_st2 + 2 * tq;
 #pragma unroll
             for (int kk = 0; kk < KD; ++kk) {
-                qb[nt][kk][0] = vb ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
-                qb[nt][kk][1] = vb ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
+                const uint16_t* src = seg + q_off[nt] + 16 * kk;
+                qb[nt][kk][0] = q_in[nt] ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+                qb[nt][kk][1] = q_in[nt] ? __ldg(reinterpret_cast<const uint32_t*>(src + 8)) : 0u;
             }
         }
     };
@@ -255,10 +277,12 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 l_run[nt][j] = 0.f;
             }
     };
-    float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN);  // [warp][row][OROW]
+    float* join = reinterpret_cast<float*>(smem + C::OFF_JOIN + team * C::JOIN);  // [warp][row][OROW]
 
     // One output row element group (four columns at d of row r): O / l and LSE, or the
-    // state that joins the shared prefix's.
+    // state that joins the shared prefix's.  (Divisions by q_len and of list positions are
+    // kept out of the pieces' code: it is run a few times a CTA, and fetching it from a
+    // busy memory takes longer than running it.)
     auto write_out = [&](int b, int hk, int r, int d, bool shared, float M, float L, const float (&v)[4]) {
         if (shared) {
             const int64_t row = ((int64_t)b * p.Hkv + hk) * p.rows + r;
@@ -266,24 +290,25 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
             if (d == 0) *reinterpret_cast<float2*>(p.own_ml + row * 2) = make_float2(M, L);
             return;
         }
-        const int hq = hk * p.G + r / p.q_len, i = r % p.q_len;
         const bool some = L > 0.f && M != -INFINITY;
         const float inv = some ? 1.0f / L : 0.f;
+        const int hq = hk * p.G + sh.row_at[r] / 256, i = sh.row_at[r] % 256;
         uint16_t* o = p.o + (int64_t)b * p.o_st0 + (int64_t)hq * p.o_st1 + (int64_t)i * p.o_st2 + d;
         // a row that attends nothing: O = 0
         *reinterpret_cast<uint2*>(o) =
             some || L != L ? make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv))
                            : make_uint2(0u, 0u);
         if (d == 0 && p.lse)
-            p.lse[((int64_t)b * p.Hq + hq) * p.q_len + i] = some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+            p.lse[((int64_t)b * p.Hq + hq) * p.q_len + i] =
+                some ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
     };
 
     // The end of a piece: the warps' states joined, and written out if it is a whole
-    // segment, else left as a partial result.
-    auto end_piece = [&](const PdWalk& at, int c0, int c1) {
+    // segment, else left as partial result `part`.
+    auto end_piece = [&](const PdWalk& at, int part) {
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
-            compute_sync();  // the buffer's last states have been read
+            team_sync(team);  // the buffer's last states have been read
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float l = l_run[nt][j];  // sum over the eight key groups
@@ -291,41 +316,41 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
                 if (g == 0) {
-                    sh.m[warp][2 * tq + j] = m_run[nt][j];
-                    sh.l[warp][2 * tq + j] = l;
+                    sh.m[team][tw][2 * tq + j] = m_run[nt][j];
+                    sh.l[team][tw][2 * tq + j] = l;
                 }
-                float* dst = join + (warp * 8 + 2 * tq + j) * C::OROW + g;
+                float* dst = join + (tw * 8 + 2 * tq + j) * C::OROW + g;
 #pragma unroll
                 for (int mt = 0; mt < KD; ++mt) {
                     dst[16 * mt] = oacc[mt][nt][j];
                     dst[16 * mt + 8] = oacc[mt][nt][2 + j];
                 }
             }
-            compute_sync();
+            team_sync(team);
             const int items = min(8, p.rows - 8 * nt) * (D / 4);
-            for (int it = threadIdx.x; it < items; it += 32 * kPdWarps) {
+            for (int it = tid; it < items; it += 32 * kPdWarps) {
                 const int r8 = it / (D / 4), r = 8 * nt + r8, d = (it % (D / 4)) * 4;
                 float M = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < kPdWarps; ++k) M = fmaxf(M, sh.m[k][r8]);
+                for (int k = 0; k < kPdWarps; ++k) M = fmaxf(M, sh.m[team][k][r8]);
                 const float Mu = M == -INFINITY ? 0.f : M;
                 float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < kPdWarps; ++k) {
-                    const float f = ex2_approx(sh.m[k][r8] - Mu);
+                    const float f = ex2_approx(sh.m[team][k][r8] - Mu);
                     const float4 x = *reinterpret_cast<const float4*>(join + (k * 8 + r8) * C::OROW + d);
-                    L = fmaf(sh.l[k][r8], f, L);
+                    L = fmaf(sh.l[team][k][r8], f, L);
                     v[0] = fmaf(x.x, f, v[0]);
                     v[1] = fmaf(x.y, f, v[1]);
                     v[2] = fmaf(x.z, f, v[2]);
                     v[3] = fmaf(x.w, f, v[3]);
                 }
-                if (c0 == c1) {
+                if (part < 0) {
                     write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
                 } else {
-                    const int64_t part = (2 * (int64_t)blockIdx.x + (c0 == (int)blockIdx.x)) * p.rows + r;
-                    __stcg(reinterpret_cast<float4*>(p.part_o + part * D + d), make_float4(v[0], v[1], v[2], v[3]));
-                    if (d == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + part * 2), make_float2(M, L));
+                    const int64_t row = (int64_t)part * p.rows + r;
+                    __stcg(reinterpret_cast<float4*>(p.part_o + row * D + d), make_float4(v[0], v[1], v[2], v[3]));
+                    if (d == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + row * 2), make_float2(M, L));
                 }
             }
         }
@@ -336,12 +361,12 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     // of one) can be split; both arrive at the share's end, where the fence's and the
     // counters' latency holds up nothing.
     auto join_parts = [&](const PdWalk& at, int c0, int c1) {
-        for (int it = threadIdx.x; it < p.rows * (D / 4); it += 32 * kPdWarps) {
+        for (int it = tid; it < p.rows * (D / 4); it += 32 * kPdWarps) {
             const int r = it / (D / 4), d = (it % (D / 4)) * 4;
             const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + r;
             const float* po = p.part_o + (int64_t)r * D + d;
             float M = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(ml + (2 * (int64_t)c + (c == c0)) * p.rows).x);
             const float Mu = M == -INFINITY ? 0.f : M;
             float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -362,66 +387,61 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     };
 
     const float F = SCORE == FA_SCORE_SOFTCAP ? p.softcap * kLog2e : p.scale * kLog2e;
-    // One page: the warp's 16 keys, the first of them kv0.  kEarly: all of their K and V is
-    // taken to registers first and the ring's slot given back before the products.
-    constexpr bool kEarly = !(D == 128 && NR == 2);
-    auto page = [&](uint32_t kbase, uint32_t vbase, int kv0, int pos0, int pos1, bool edge, uint64_t* freed) {
-        uint32_t ka[kEarly ? KD : 1][4], va[kEarly ? KD : 1][4];
-        if constexpr (kEarly) {
+    // One page: the warp's 32 keys, the first of them kv0.  K's slot is given back after its
+    // products; V's tile is waited for when it is needed.
+    auto page = [&](uint32_t kbase, uint32_t vbase, int kv0, int pos0, int pos1, bool edge, uint64_t* k_free,
+                    uint64_t* v_full, uint32_t v_phase) {
+        float sacc[2][NR][4];
 #pragma unroll
-            for (int kk = 0; kk < KD; ++kk)
-                ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[kk]);
-#pragma unroll
-            for (int mt = 0; mt < KD; ++mt)
-                ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[mt]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(freed);
-        }
-        float sacc[NR][4], sodd[NR][4];  // two chains of products
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[nt][e] = sodd[nt][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < KD; ++kk) {
-            if constexpr (!kEarly)
-                ldsm_x4(swz(kbase, key0 + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka[0]);
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
-                mma_bf16_16816(kk & 1 ? sodd[nt] : sacc[nt], ka[kEarly ? kk : 0], qb[nt][kk][0], qb[nt][kk][1]);
-        }
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
+                for (int e = 0; e < 4; ++e) sacc[kt][nt][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[nt][e] += sodd[nt][e];
+        for (int kk = 0; kk < KD; ++kk)
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                uint32_t ka[4];
+                ldsm_x4(swz(kbase, key0 + 16 * kt + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka);
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(sacc[kt][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+            }
+
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_free);
+
         if constexpr (SCORE == FA_SCORE_SOFTCAP) {
             // tanh: the polynomial, and the far form where the warp has a far score
             bool far = false;
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
+            for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sacc[nt][e] *= p.softcap_in;
-                    far |= fabsf(sacc[nt][e]) > kTanhPolyMax;
-                }
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sacc[kt][nt][e] *= p.softcap_in;
+                        far |= fabsf(sacc[kt][nt][e]) > kTanhPolyMax;
+                    }
             const bool any = __any_sync(0xFFFFFFFFu, far);
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
+            for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float y0 = sacc[nt][e], y1 = sacc[nt][e + 1];
-                    float t0, t1;
-                    f2_unpack(tanh_poly2(f2_pack(y0, y1)), t0, t1);
-                    if (any) {
-                        const float u0 = tanh_far(y0), u1 = tanh_far(y1);
-                        t0 = fabsf(y0) > kTanhPolyMax ? u0 : t0;
-                        t1 = fabsf(y1) > kTanhPolyMax ? u1 : t1;
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float y0 = sacc[kt][nt][e], y1 = sacc[kt][nt][e + 1];
+                        float t0, t1;
+                        f2_unpack(tanh_poly2(f2_pack(y0, y1)), t0, t1);
+                        if (any) {
+                            const float u0 = tanh_far(y0), u1 = tanh_far(y1);
+                            t0 = fabsf(y0) > kTanhPolyMax ? u0 : t0;
+                            t1 = fabsf(y1) > kTanhPolyMax ? u1 : t1;
+                        }
+                        sacc[kt][nt][e] = t0;
+                        sacc[kt][nt][e + 1] = t1;
                     }
-                    sacc[nt][e] = t0;
-                    sacc[nt][e + 1] = t1;
-                }
         }
-
         // score_mod in log2 units; masked scores are replaced
         float mt_[NR][2];
 #pragma unroll
@@ -431,20 +451,22 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = e & 1;
-                const int kv = kv0 + g + 8 * (e >> 1);
-                const int pos = pos0 + tok[nt][j];
-                bool adm = rvalid[nt][j];
-                if (edge) adm = adm && kv <= pos && (!p.has_window || (int64_t)pos - kv <= p.window);
-                float x = sacc[nt][e];
-                if constexpr (SCORE == FA_SCORE_SOFTCAP) x = x * F;  // capped above
-                else if constexpr (SCORE == FA_SCORE_ALIBI) x = fmaf(slope[nt][j], (float)(kv - pos), x * F);
-                else x = x * F;
-                x = adm ? x : -INFINITY;
-                sacc[nt][e] = x;
-                mt_[nt][j] = fmaxf(mt_[nt][j], x);
-            }
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = e & 1;
+                    const int kv = kv0 + 16 * kt + g + 8 * (e >> 1);
+                    const int pos = pos0 + tok[nt][j];
+                    bool adm = rvalid[nt][j];
+                    if (edge) adm = adm && kv <= pos && (!p.has_window || (int64_t)pos - kv <= p.window);
+                    float x = sacc[kt][nt][e];
+                    if constexpr (SCORE == FA_SCORE_SOFTCAP) x = x * F;  // capped above
+                    else if constexpr (SCORE == FA_SCORE_ALIBI) x = fmaf(slope[nt][j], (float)(kv - pos), x * F);
+                    else x = x * F;
+                    x = adm ? x : -INFINITY;
+                    sacc[kt][nt][e] = x;
+                    mt_[nt][j] = fmaxf(mt_[nt][j], x);
+                }
         float alpha[NR][2], m_use[NR][2];
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
@@ -460,95 +482,117 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 m_run[nt][j] = m_new;
                 l_run[nt][j] *= alpha[nt][j];
             }
-        // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor core's operand
-        // type); the sum is taken of the unrounded values
-        uint32_t pb[NR][2];
+        // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor
+        // core's operand type); the sum is taken of the unrounded values
+        uint32_t pb[2][NR][2];
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt) {
-            float pv[4];
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pv[e] = ex2_approx(sacc[nt][e] - m_use[nt][e & 1]);
-                l_run[nt][e & 1] += pv[e];
+            for (int nt = 0; nt < NR; ++nt) {
+                float pv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    pv[e] = ex2_approx(sacc[kt][nt][e] - m_use[nt][e & 1]);
+                    l_run[nt][e & 1] += pv[e];
+                }
+                pb[kt][nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
+                pb[kt][nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
             }
-            pb[nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
-            pb[nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
-        }
 #pragma unroll
         for (int mt = 0; mt < KD; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
+        // after a timeout V's tile may not have landed: whatever it holds
+        __all_sync(0xFFFFFFFFu, mbar_wait(v_full, v_phase, wd));
+        // V^T of 16 columns (mt) and 16 keys (kt)
+        auto load_v = [&](int mt, int kt, uint32_t (&va)[4]) {
+            ldsm_x4_trans(swz(vbase, key0 + 16 * kt + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va);
+        };
         if (!edge) {
 #pragma unroll
-            for (int mt = 0; mt < KD; ++mt) {
-                if constexpr (!kEarly)
-                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va[0]);
+            for (int mt = 0; mt < KD; ++mt)
 #pragma unroll
-                for (int nt = 0; nt < NR; ++nt)
-                    mma_bf16_16816(oacc[mt][nt], va[kEarly ? mt : 0], pb[nt][0], pb[nt][1]);
-            }
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t va[4];
+                    load_v(mt, kt, va);
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt)
+                        mma_bf16_16816(oacc[mt][nt], va, pb[kt][nt][0], pb[kt][nt][1]);
+                }
         } else {
             // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the
             // same + 8 that a row at positions [from, to] may attend
-            auto keep = [&](int from, int to, uint32_t (&k2)[2]) {
+            auto keep = [&](int kt, int from, int to, uint32_t (&k2)[2]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int kv = kv0 + 2 * tq + 8 * h;
+                    const int kv = kv0 + 16 * kt + 2 * tq + 8 * h;
                     const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
                     const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
                     k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
                 }
             };
-            uint32_t any2[2];
-            keep(pos0, pos1, any2);
+            uint32_t k2[2][2];
 #pragma unroll
-            for (int mt = 0; mt < KD; ++mt) {
-                uint32_t vr[4];
-                if constexpr (!kEarly) {
-                    ldsm_x4_trans(swz(vbase, key0 + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), vr);
-                } else {
+            for (int kt = 0; kt < 2; ++kt) keep(kt, pos0, pos1, k2[kt]);
+            // an infinity or NaN that some rows attend and others may not: one product per
+            // token, each with its own keys, kept for its rows only
+            bool odd = false;
+            if (p.q_len > 1) {
+#pragma unroll 1
+                for (int mt = 0; mt < KD; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) vr[e] = va[mt][e];
-                }
-                bool odd = false;
+                    for (int kt = 0; kt < 2; ++kt) {
+                        uint32_t vr[4];
+                        load_v(mt, kt, vr);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    vr[e] &= any2[e >> 1];
-                    odd |= nonfinite2(vr[e]);
-                }
-                if (p.q_len > 1 && __any_sync(0xFFFFFFFFu, odd)) {
-                    // an infinity or NaN that some rows attend and others may not: one
-                    // product per token, each with its own keys, kept for its rows only
-                    for (int i = 0; i < p.q_len; ++i) {
-                        uint32_t k2[2], vi[4];
-                        keep(pos0 + i, pos0 + i, k2);
+                        for (int e = 0; e < 4; ++e) odd |= nonfinite2(vr[e] & k2[kt][e >> 1]);
+                    }
+                odd = __any_sync(0xFFFFFFFFu, odd);
+            }
+            const int passes = odd ? p.q_len : 1;
+#pragma unroll 1
+            for (int t = 0; t < passes; ++t) {
+                if (odd)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) vi[e] = vr[e] & k2[e >> 1];
+                    for (int kt = 0; kt < 2; ++kt) keep(kt, pos0 + t, pos0 + t, k2[kt]);
+#pragma unroll
+                for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt) {
+                        uint32_t vr[4];
+                        load_v(mt, kt, vr);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) vr[e] &= k2[kt][e >> 1];
 #pragma unroll
                         for (int nt = 0; nt < NR; ++nt) {
-                            float d4[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_bf16_16816(d4, vi, pb[nt][0], pb[nt][1]);
+                            float d4[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) d4[e] = oacc[mt][nt][e];
+                            mma_bf16_16816(d4, vr, pb[kt][nt][0], pb[kt][nt][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (tok[nt][e & 1] == i) oacc[mt][nt][e] += d4[e];
+                                if (!odd || tok[nt][e & 1] == t) oacc[mt][nt][e] = d4[e];
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(oacc[mt][nt], vr, pb[nt][0], pb[nt][1]);
-                }
             }
         }
     };
 
-    // the share's first and last piece where they are parts of a split segment
+    // the share's first and last piece where they are parts of a split segment, and the
+    // list positions of those segments
     PdWalk head = w, tail = w;
-    int head0 = -1, head1 = -1, tail0 = -1, tail1 = -1;
+    long long xhead = -1, xtail = -1;
     if (count > 0) load_segment(w.b, w.hk);
     long long xseg = x0 - w.t;  // list position of the segment's first page
-    uint32_t slot = 0, phase = 0;
+    uint32_t slot = 0, phase = 0;  // of the next tile
+    auto step = [&]() {
+        if (++slot == C::NT) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
     for (int done = 0; done < count;) {
         // a piece: pages [w.t, w.t + n) of the segment
         const int n = min(w.r.n - w.t, count - done);
@@ -558,73 +602,76 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         for (int i = 0; i < n; ++i, kv0 += 128) {
             // after a timeout the warp still walks its share (without computing), so that
             // the pieces' barriers and counters stay whole
-            if (__all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[slot], phase, wd))) {
-                const uint32_t kbase = smem_u32(smem + slot * C::STAGE), vbase = kbase + C::TILE;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], phase, wd));
+            const uint32_t ks = slot;
+            step();
+            if (ok) {
+                const uint32_t kbase = smem_u32(ring + ks * C::TILE), vbase = smem_u32(ring + slot * C::TILE);
                 // no row attends any of the warp's keys, or some row not all of them
-                const bool none = kv0 > pos1 || (p.has_window && kv0 + 15 < pos0 - p.window);
-                const bool edge = kv0 + 15 > pos0 || (p.has_window && kv0 < pos1 - p.window);
-                if (!none) page(kbase, vbase, kv0, pos0, pos1, edge, &sh.empty[slot]);
-                if (none || !kEarly) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                const bool none = kv0 > pos1 || (p.has_window && kv0 + 31 < pos0 - p.window);
+                const bool edge = kv0 + 31 > pos0 || (p.has_window && kv0 < pos1 - p.window);
+                if (!none) {
+                    page(kbase, vbase, kv0, pos0, pos1, edge, &empty[ks], &full[slot], phase);
+                } else {
+                    if (lane == 0) mbar_arrive(&empty[ks]);
+                    __all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], phase, wd));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
             }
-            if (++slot == C::NS) {
-                slot = 0;
-                phase ^= 1;
-            }
+            step();
         }
         done += n;
-        const int c0 = pd_holder(T, xseg, used), c1 = pd_holder(T, xseg + w.r.n - 1, used);
         PdWalk next = w;
         next.t += n - 1;
         if (done < count) {
             pd_advance(p, next, bad);
             load_segment(next.b, next.hk);  // its latency passes during the join
         }
-        end_piece(w, c0, c1);
-        if (c0 != c1) {
-            if (xseg < x0) {
-                head = w;
-                head0 = c0;
-                head1 = c1;
-            } else {
-                tail = w;
-                tail0 = c0;
-                tail1 = c1;
-            }
+        int part = -1;
+        if (xseg < x0) {  // the segment's first piece is another team's
+            head = w;
+            xhead = xseg;
+            part = 2 * me;
+        } else if (xseg + w.r.n > x0 + count) {  // only its first piece is here
+            tail = w;
+            xtail = xseg;
+            part = 2 * me + 1;
         }
+        end_piece(w, part);
         xseg += w.r.n;
         w = next;
     }
-    if (head0 >= 0 || tail0 >= 0) {
-        compute_sync();
-        if (threadIdx.x == 0) {
+    if (xhead >= 0 || xtail >= 0) {
+        team_sync(team);
+        const int h0 = xhead >= 0 ? pd_holder(T, xhead, used) : 0;
+        const int h1 = xhead >= 0 ? pd_holder(T, xhead + head.r.n - 1, used) : 0;
+        const int t1 = xtail >= 0 ? pd_holder(T, xtail + tail.r.n - 1, used) : 0;
+        if (tid == 0) {
             __threadfence();
-            const unsigned nh = (unsigned)(head1 - head0), nt = (unsigned)(tail1 - tail0);
             unsigned h = 0, t = 0;  // the counters wrap to zero at the last piece
-            if (head0 >= 0) h = atomicInc(p.arrived + head0, nh);
-            if (tail0 >= 0) t = atomicInc(p.arrived + tail0, nt);
-            sh.last[0] = head0 >= 0 && h == nh;
-            sh.last[1] = tail0 >= 0 && t == nt;
+            if (xhead >= 0) h = atomicInc(p.arrived + h0, (unsigned)(h1 - h0));
+            if (xtail >= 0) t = atomicInc(p.arrived + me, (unsigned)(t1 - me));
+            sh.last[team][0] = xhead >= 0 && h == (unsigned)(h1 - h0);
+            sh.last[team][1] = xtail >= 0 && t == (unsigned)(t1 - me);
             __threadfence();
         }
-        compute_sync();
-        if (sh.last[0]) join_parts(head, head0, head1);
-        if (sh.last[1]) join_parts(tail, tail0, tail1);
+        team_sync(team);
+        if (sh.last[team][0]) join_parts(head, h0, h1);
+        if (sh.last[team][1]) join_parts(tail, me, t1);
     }
     // sequences without a key: O = 0, LSE = -inf
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (pd_range(p, __ldg(p.seq_lens + b), bad).n > 0) continue;
         const int per_head = p.q_len * (D / 8);
-        for (int it = threadIdx.x; it < p.Hq * per_head; it += 32 * kPdWarps) {
+        for (int it = threadIdx.x; it < p.Hq * per_head; it += 32 * kPdWarps * kPdTeams) {
             const int h = it / per_head, i = it % per_head / (D / 8), u = it % (D / 8);
             uint16_t* o = p.o + (int64_t)b * p.o_st0 + (int64_t)h * p.o_st1 + (int64_t)i * p.o_st2;
             reinterpret_cast<uint4*>(o)[u] = make_uint4(0, 0, 0, 0);
             if (u == 0 && p.lse) p.lse[((int64_t)b * p.Hq + h) * p.q_len + i] = -INFINITY;
         }
     }
-    if (bad && threadIdx.x < 32 * kPdWarps) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
+    if (bad) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
     if (wd.failed && lane == 0) atomicOr(p.status, STATUS_TIMEOUT);
     // behind a shared prefix's kernel: this grid does not end before it, so that the join
     // finds both done

@@ -8,8 +8,9 @@
 
 namespace fa {
 
-constexpr int kPdWarps = 8;                       // compute warps of a CTA, 16 keys of a page each
-constexpr int kPdThreads = 32 * (kPdWarps + 1);   // and the TMA producer warp
+constexpr int kPdTeams = 2;                       // of a CTA, each with a share of the work
+constexpr int kPdWarps = 4;                       // compute warps of a team, 32 keys of a page each
+constexpr int kPdThreads = 32 * kPdTeams * (kPdWarps + 1);  // and a TMA producer warp each
 constexpr int kPdMaxRows = 16;                    // query rows of a kv head's group: G * q_len
 
 struct PdParams {
@@ -35,13 +36,13 @@ struct PdParams {
     float softcap, softcap_in;
     const float* slopes;
 
-    // Work split: CTA c of `grid` takes the c-th share of the list of pages.  A segment
-    // split over CTAs c0..c1 leaves partial results 2 c0 + 1 (its first piece, the end of
+    // Work split: team c of `teams` takes the c-th share of the list of pages.  A segment
+    // split over teams c0..c1 leaves partial results 2 c0 + 1 (its first piece, the end of
     // c0's share) and 2 c for c in (c0, c1] (the start of c's share)
-    int32_t grid;
-    float* part_o;        // [2 * grid][rows][D] fp32, unnormalised
-    float* part_ml;       // [2 * grid][rows][2]: running max (log2 units), sum
-    unsigned* arrived;    // [grid] pieces done of the segment whose first piece ends share c0;
+    int32_t grid, teams;  // CTAs, and at most kPdTeams of each
+    float* part_o;        // [2 * teams][rows][D] fp32, unnormalised
+    float* part_ml;       // [2 * teams][rows][2]: running max (log2 units), sum
+    unsigned* arrived;    // [teams] pieces done of the segment whose first piece ends share c0;
                           // every call leaves zeros
 
     // With a shared prefix: the state (log2 max, sum, unnormalised O) of the rows whose

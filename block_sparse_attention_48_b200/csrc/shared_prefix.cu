@@ -56,7 +56,7 @@ struct SpCfg {
 
 struct __align__(16) SpShared {
     uint64_t full[12], empty[12];
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_empty[2], drain[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem_base;
 };
 
@@ -182,7 +182,7 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
         __syncwarp();
     };
     // O += P V of one half
-    auto values = [&](uint32_t vpos, int h, uint32_t accumulate) {
+    auto values = [&](uint32_t vpos, int h, uint32_t accumulate, bool last) {
         const uint32_t slot = vpos % C::NS, vd = v0 + slot * (uint32_t)(C::TILE >> 4) + h * kHalf;
         tc_fence_after();
         if (elect_one_sync()) {
@@ -192,6 +192,7 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
                         idesc_o, k > 0 ? 1u : accumulate);
             umma_commit(&sh.pv_done[s]);
             if (h == 1) umma_commit(&sh.empty[slot]);
+            if (last) umma_commit(&sh.o_full[s]);
         }
         __syncwarp();
     };
@@ -215,11 +216,11 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
                 ready(&sh.full[cur.v % C::NS], (cur.v / C::NS) & 1);
                 if (!ready(&sh.p_full[s][0], tile & 1)) break;
                 if (i == 0 && piece > 0 && !ready(&sh.o_empty[s], (piece - 1) & 1)) break;
-                values(cur.v, 0, i > 0 ? 1u : 0u);
+                values(cur.v, 0, i > 0 ? 1u : 0u, false);
                 if (more && !ready(&sh.full[nx.k % C::NS], (nx.k / C::NS) & 1)) break;
                 if (more) scores(nx.k, 0);
                 if (!ready(&sh.p_full[s][1], tile & 1)) break;
-                values(cur.v, 1, 1u);
+                values(cur.v, 1, 1u, !more);
                 if (more) scores(nx.k, 1);
                 if (both) pass(at - 1 - s);
                 cur = nx;
@@ -426,10 +427,9 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
             }
         }
         if (!ok) break;
-        // the piece's last two P V (and so all its products), one phase after the other: of
-        // an earlier one than the next a parity tells nothing
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 2) & 1, wd)) &&
-             __all_sync(0xFFFFFFFFu, mbar_wait(&sh.pv_done[s], (2 * tile - 1) & 1, wd));
+        // The piece's products are done.  (Not by pv_done: whether its last phase or the one
+        // before it has ended, its parity cannot tell here.)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_full[s], piece & 1, wd));
         if (!ok) break;
         ++piece;
         tc_fence_after();
@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
                 mbar_init(&sh.p_full[s][h], 4);
             }
             mbar_init(&sh.pv_done[s], 1);
+            mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.o_empty[s], 4);
             mbar_init(&sh.drain[s], 1);
         }
