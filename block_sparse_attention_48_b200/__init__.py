@@ -25,6 +25,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -141,7 +142,18 @@ def _load():
     return lib
 
 
+def _load_packed():
+    """The serving calls with plain pointer arguments, which take a descriptor packed into
+    bytes: a step's call is short enough on the GPU for the binding's time to count."""
+    lib = ctypes.CDLL(LIB_PATH)
+    for name in ("fa_rope_apply", "fa_paged_append", "fa_decode_paged", "fa_decode_shared"):
+        getattr(lib, name).argtypes = [ctypes.c_void_p if hasattr(t, "contents") else t
+                                       for t in getattr(_lib, name).argtypes]
+    return lib
+
+
 _lib = _load()
+_packed = _load_packed()
 
 
 def library() -> ctypes.CDLL:
@@ -501,7 +513,10 @@ def flex_attention_autograd(q, k, v, block_mask: BlockMask, score_mod=None, scal
 
 # ------------------------------------------------------------------ rotary positions, paged cache
 
-_I64x4 = ctypes.c_int64 * 4
+_pack_tensor = struct.Struct("P8q").pack  # TensorDesc and RopeDesc as bytes
+_pack_rope = struct.Struct("Piif4x").pack
+assert struct.calcsize("P8q") == ctypes.sizeof(TensorDesc) and struct.calcsize("Piif4x") == ctypes.sizeof(RopeDesc)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
 
 
 def _placed(fn):
@@ -511,50 +526,52 @@ def _placed(fn):
     def call(x, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
         if not (isinstance(x, torch.Tensor) and x.is_cuda):
             raise TypeError(f"{fn.__name__}: expected CUDA tensors")
-        if stream is not None:
-            if stream.device != x.device:
-                raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
-            with torch.cuda.stream(stream):
-                return fn(x, *args, **kw)
-        if x.device.index != torch.cuda.current_device():
+        if stream is None and x.get_device() == torch._C._cuda_getDevice():
+            return fn(x, *args, **kw)
+        if stream is None:
             with torch.cuda.device(x.device):
                 return fn(x, *args, **kw)
-        return fn(x, *args, **kw)
+        if stream.device != x.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
+        with torch.cuda.stream(stream):
+            return fn(x, *args, **kw)
     return call
 
 
 def _readable(t: torch.Tensor) -> torch.Tensor:
     """t itself, or a contiguous copy where its strides or alignment are not ones the
     kernels read (16-byte vectors along D, no expanded dimension)."""
-    if t.dim() == 4 and t.numel():
-        st = t.stride()
-        if st[3] != 1 or (st[0] | st[1] | st[2]) & 7 or t.data_ptr() & 15 or (0 in st and _expanded(t)):
+    if t.dim() == 4:
+        s0, s1, s2, s3 = t.stride()
+        if (s3 != 1 or (s0 | s1 | s2) & 7 or t.data_ptr() & 15 or not (s0 and s1 and s2)) and t.numel() and \
+                (s3 != 1 or (s0 | s1 | s2) & 7 or t.data_ptr() & 15 or _expanded(t)):
             return t.contiguous() if not t.is_contiguous() else t.clone()
     return t
 
 
-def _desc(t: torch.Tensor, device: torch.device, what: str) -> TensorDesc:
-    if t.dtype != torch.bfloat16 or t.dim() != 4 or t.device != device:
+def _desc(t: torch.Tensor, device: torch.device, what: str) -> bytes:
+    if t.dtype is not torch.bfloat16 or t.dim() != 4 or t.device != device:
         raise TypeError(f"{what}: expected a 4-D bf16 tensor on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return TensorDesc(t.data_ptr(), _I64x4(*t.shape), _I64x4(*t.stride()))
+    return _pack_tensor(t.data_ptr(), *t.shape, *t.stride())
 
 
 def _ints(t: torch.Tensor, shape: tuple, device: torch.device, what: str) -> int:
     """Address of an int32 tensor of the given shape (None: any size), its last dimension contiguous."""
-    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)) or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    have = t.shape
+    if t.dtype is not torch.int32 or t.device != device or len(have) != len(shape) or have[0] != shape[0] or \
+            (shape[-1] is not None and have[-1] != shape[-1]) or (t.stride(-1) != 1 and have[-1] > 1):
         raise TypeError(f"{what}: expected int32 {list(shape)} on {device} with a contiguous last dimension, "
                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, amplitude: float, device: torch.device) -> RopeDesc:
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
+def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, amplitude: float, device: torch.device) -> bytes:
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
             (inv_freq.shape[0] > 1 and inv_freq.stride(0) != 1):
         raise TypeError(f"inv_freq: expected a contiguous fp64 tensor [rotary_dim / 2] on {device}")
     if not amplitude > 0:
         raise ValueError("amplitude must be positive")
-    return RopeDesc(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude)
+    return _pack_rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude)
 
 
 _paged_workspaces = {}
@@ -570,7 +587,7 @@ def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros((max(need, _STATUS_BYTES),), dtype=torch.uint8, device=device)
     index = device.index if device.index is not None else torch.cuda.current_device()
-    kept = _paged_workspaces.setdefault((index, torch.cuda.current_stream(index).cuda_stream), [])
+    kept = _paged_workspaces.setdefault((index, _raw_stream(index)), [])
     if not kept or kept[-1].numel() < need:
         ws = torch.zeros((max(need, 1 << 22),), dtype=torch.uint8, device=device)
         if kept:
@@ -634,8 +651,8 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tenso
         B, S = q.shape[0], q.shape[2]
         pos = _ints(positions, (S,) if positions.dim() == 1 else (B, S), device, "positions")
         pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    _check(_lib.fa_rope_apply(qd, kd, rope, pos, pos_stride, offset, 1 if inverse else 0, qo, ko,
-                              torch.cuda.current_stream().cuda_stream), "fa_rope_apply")
+    _check(_packed.fa_rope_apply(qd, kd, rope, pos, pos_stride, offset, 1 if inverse else 0, qo, ko,
+                                 _raw_stream(device.index)), "fa_rope_apply")
     return out
 
 
@@ -694,9 +711,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     elif q_out is not None:
         raise ValueError("paged_append: q_out without q")
     ws = paged_workspace(device) if ws is None else _given_workspace(ws, _STATUS_BYTES, device, "fa_paged_append")
-    _check(_lib.fa_paged_append(kd, vd, qd, rope, have, fresh, table, page_table.stride(0), page_table.shape[1], kp, vp,
-                                qo, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream),
-           "fa_paged_append")
+    _check(_packed.fa_paged_append(kd, vd, qd, rope, have, fresh, table, page_table.stride(0), page_table.shape[1], kp,
+                                   vp, qo, ws.data_ptr(), ws.numel(), _raw_stream(device.index)), "fa_paged_append")
     return q_out
 
 
@@ -719,10 +735,11 @@ def _decode_pages(name, fn, need, q, k_pages, v_pages, page_table, seq_lens, ext
         sm, _ = score_mod_desc(score_mod)
         if score_mod[0] == "alibi" and (score_mod[1].shape != (Hq,) or score_mod[1].device != device):
             raise TypeError(f"ALiBi slopes: fp32 [Hq] on {device}")
+        sm = bytes(sm)
     ws = paged_workspace(device, need) if ws is None else _given_workspace(ws, need, device, name)
     _check(fn(qd, kp, vp, table, page_table.stride(0), page_table.shape[1], lens, extra, sm,
               scale if scale is not None else 0.0, od, lse.data_ptr(), ws.data_ptr(), ws.numel(),
-              torch.cuda.current_stream().cuda_stream), name)
+              _raw_stream(device.index)), name)
     return out, lse
 
 
@@ -740,7 +757,7 @@ def flex_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     if window is not None and window < 0:
         raise ValueError("flex_decode_paged: window must not be negative")
     need = int(_lib.fa_decode_paged_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3]))
-    return _decode_pages("fa_decode_paged", _lib.fa_decode_paged, need, q, k_pages, v_pages, page_table, seq_lens,
+    return _decode_pages("fa_decode_paged", _packed.fa_decode_paged, need, q, k_pages, v_pages, page_table, seq_lens,
                          -1 if window is None else window, score_mod, scale, out, lse, ws)
 
 
@@ -754,7 +771,7 @@ def flex_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     pages), which are taken once for the whole batch (fa_decode_shared)."""
     need = int(_lib.fa_decode_shared_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3],
                                                     prefix_len))
-    return _decode_pages("fa_decode_shared", _lib.fa_decode_shared, need, q, k_pages, v_pages, page_table, seq_lens,
+    return _decode_pages("fa_decode_shared", _packed.fa_decode_shared, need, q, k_pages, v_pages, page_table, seq_lens,
                          prefix_len, score_mod, scale, out, lse, ws)
 
 
