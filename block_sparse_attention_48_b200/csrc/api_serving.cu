@@ -215,8 +215,8 @@ namespace {
 // shape, since they alone must be zero when a call starts.  With a shared prefix, the
 // prefix's partial results and every row's own state follow.
 struct PdLayout {
-    size_t arrived, ml, o, pre_ml, pre_o, own_ml, own_o, end;
-    int sms, pre_ctas;  // CTAs of a paged decode at most, CTAs of the prefix
+    size_t arrived, ml, o, split, pre_ml, pre_o, own_ml, own_o, end;
+    int sms;
 };
 
 PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
@@ -228,15 +228,15 @@ PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t pref
     L.ml = L.arrived + align256(teams * sizeof(uint32_t));
     L.o = L.ml + align256(parts * 2 * sizeof(float));
     L.end = L.o + parts * D * sizeof(float);
-    L.pre_ml = L.pre_o = L.own_ml = L.own_o = 0;
-    L.pre_ctas = 0;
+    L.split = L.pre_ml = L.pre_o = L.own_ml = L.own_o = 0;
     if (prefix_pages > 0) {
         const fa::SpGeom g = fa::sp_geom(B * rows, (int32_t)prefix_pages);
         const int64_t entries = Hkv * g.per_head;
-        L.pre_ctas = (int)(entries < (int64_t)ctas ? entries : (int64_t)ctas);
-        const size_t slots = 2 * ((size_t)Hkv * fa::sp_cols(g) + L.pre_ctas) * fa::kSpRows;
+        const size_t pre_ctas = entries < (int64_t)ctas ? (size_t)entries : ctas;
+        const size_t slots = 2 * ((size_t)Hkv * fa::sp_cols(g) + pre_ctas) * fa::kSpRows;
         const size_t own = (size_t)(B * Hkv * rows);
-        L.pre_ml = align256(L.end);
+        L.split = align256(L.end);
+        L.pre_ml = L.split + 256;
         L.pre_o = L.pre_ml + align256(slots * 2 * sizeof(float));
         L.own_ml = L.pre_o + slots * D * sizeof(float);
         L.own_o = L.own_ml + align256(own * 2 * sizeof(float));
@@ -319,6 +319,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prefix_pages == 0) return fa::launch_paged_decode(P, (int)D, kind, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 
+    if (lay.sms < 2) return FA_ERR_UNSUPPORTED;
     P.own_ml = reinterpret_cast<float*>(ws + lay.own_ml);
     P.own_o = reinterpret_cast<float*>(ws + lay.own_o);
     fa::SpParams S;
@@ -334,7 +335,10 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.scale = P.scale; S.softcap = P.softcap; S.softcap_in = P.softcap_in;
     S.slopes = P.slopes;
     S.geom = fa::sp_geom(B * P.rows, (int32_t)prefix_pages);
-    S.used = lay.pre_ctas;
+    P.sms = lay.sms;
+    P.prefix_entries = Hkv * S.geom.per_head;
+    S.sms = P.sms;
+    S.split = reinterpret_cast<int32_t*>(ws + lay.split);
     S.part_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
     S.part_o = reinterpret_cast<float*>(ws + lay.pre_o);
     S.o = P.o;
@@ -343,6 +347,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.own_o = P.own_o;
     S.own_ml = P.own_ml;
     S.pt_width = P.pt_width;
+    S.prefix_pages = P.prefix_pages;
     S.status = P.status;
     S.watchdog_ns = P.watchdog_ns;
     if (fa::launch_shared_prefix(S, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;

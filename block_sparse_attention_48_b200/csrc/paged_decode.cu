@@ -23,6 +23,7 @@
 // Places outside a row's keys may hold anything (a page's slots behind the last key
 // are not initialised, and masked keys may hold infinities or NaN): their scores are
 // replaced, not added to, and values that no row attends are zeroed before the product.
+#include <climits>
 #include <mutex>
 #include <vector>
 
@@ -34,6 +35,7 @@
 #include "flexattn.h"
 #include "paged_decode.cuh"
 #include "paged_walk.cuh"
+#include "shared_walk.cuh"
 #include "ptx.cuh"
 #include "score_math.cuh"
 
@@ -59,7 +61,7 @@ struct __align__(16) PdShared {
     uint64_t full[kPdTeams][6], empty[kPdTeams][6];
     long long scan[kPdThreads / 32];
     long long total;                          // list length
-    int used;                                 // teams that have work
+    int used, ctas;                           // teams that have work, and their CTAs
     PdWalk start[kPdTeams];                   // where a team's share starts
     int last[kPdTeams][2];                    // this team completed the split segment
     uint16_t row_at[kPdMaxRows];              // a query row's head in its group * 256 + its token
@@ -94,7 +96,10 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w)
 
 // Team of the work split: the first teams of all CTAs come before the second ones, so
 // that a short list is spread over the SMs.
-__device__ __forceinline__ int pd_team(int team) { return (int)blockIdx.x + (int)gridDim.x * team; }
+__device__ __forceinline__ int pd_team(int ctas, int team)
+{
+    return (int)blockIdx.x < ctas ? (int)blockIdx.x + ctas * team : INT_MAX;
+}
 
 // All threads: the list's length and where this CTA's shares start.
 __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool& bad)
@@ -118,15 +123,18 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
         total += sh.scan[w];
     }
     const long long T = total * p.Hkv;
-    const int used = (int)min(T, (long long)p.teams);
+    // beside a shared prefix, the CTAs that its kernel leaves SMs to
+    const int ctas = p.prefix_entries ? min(p.grid, p.sms - sp_split(p.prefix_entries, T, p.sms)) : p.grid;
+    const int used = (int)min(T, (long long)min(p.teams, ctas * kPdTeams));
     if (tid == 0) {
         sh.total = T;
         sh.used = used;
+        sh.ctas = ctas;
     }
 #pragma unroll
     for (int team = 0; team < kPdTeams; ++team) {
-        if (pd_team(team) >= used) continue;
-        const long long x0 = pd_share(T, pd_team(team), used);
+        if (pd_team(ctas, team) >= used) continue;
+        const long long x0 = pd_share(T, pd_team(ctas, team), used);
         const long long acc = before + inc - mine;  // pages of the sequences before this thread's
         if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + mine)) pd_find(p, x0, lo, hi, acc, sh.start[team], bad);
     }
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
         sh.row_at[threadIdx.x] = (uint16_t)(threadIdx.x / p.q_len * 256 + threadIdx.x % p.q_len);
     pd_locate(p, sh, bad);  // ends with a CTA barrier
     const int team = warp < kPdTeams * kPdWarps ? warp / kPdWarps : warp - kPdTeams * kPdWarps;
-    const int me = pd_team(team);
+    const int me = pd_team(sh.ctas, team);
     uint64_t *full = sh.full[team], *empty = sh.empty[team];
     uint8_t* ring = smem + team * C::NT * C::TILE;
     const long long T = sh.total;

@@ -9,8 +9,10 @@
 //
 // K and V of the prefix are read once for up to 256 rows, so the bound goes from HBM
 // (few rows) to the tensor cores and the exponentials (4 D flops and one exponential per
-// row and key).  A CTA per SM takes an equal share of the list of column entries
-// (shared_walk.cuh).  K and V tiles arrive by TMA in one ring.  Two streams, each a tile
+// row and key).  CTA c of those that the prefix gets takes the c-th equal share of the
+// list of column entries (shared_walk.cuh); the other SMs run the paged decode of the
+// sequences' own pages, which is bound by HBM, meanwhile (one after the other, each on
+// all SMs: 104 us where both together take 80).  K and V tiles arrive by TMA in one ring.  Two streams, each a tile
 // of 128 rows with its own MMA warp and four softmax warps, share the tensor cores and
 // the exponential units.  S, P (over S) and O live in tensor memory; a thread owns a
 // row.  A tile is taken in halves of 64 keys with a buffer each: while one half's scores
@@ -58,6 +60,7 @@ struct __align__(16) SpShared {
     uint64_t full[12], empty[12];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem_base;
+    long long pages[kSpThreads / 32];  // of the sequences' own, by warp
 };
 
 // Ring positions of an entry's tiles for a stream: K at `k`, V at `v`.
@@ -461,6 +464,16 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32;
     launch_dependents();
+    // the sequences' own pages, which decide how many SMs the prefix gets (a bad length is
+    // reported by the paged decode)
+    long long own = 0;
+    {
+        bool bad = false;
+        for (int b = threadIdx.x; b < p.B; b += kSpThreads) own += pd_range(p, __ldg(p.seq_lens + b), bad).n;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xFFFFFFFFu, own, o);
+        if (threadIdx.x % 32 == 0) sh.pages[warp] = own;
+    }
     if (warp == kMmaWarp) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
@@ -488,7 +501,14 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const long long T = (long long)p.Hkv * p.geom.per_head;
-    const long long x0 = pd_share(T, blockIdx.x, p.used), x1 = pd_share(T, blockIdx.x + 1, p.used);
+    own = 0;
+#pragma unroll
+    for (int w = 0; w < kSpThreads / 32; ++w) own += sh.pages[w];
+    const int used = sp_split(T, own * p.Hkv, p.sms);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.split = used;
+    const bool works = (int)blockIdx.x < used;
+    const long long x0 = works ? pd_share(T, blockIdx.x, used) : 0;
+    const long long x1 = works ? pd_share(T, blockIdx.x + 1, used) : 0;
     Watchdog wd{p.watchdog_ns, false};
     if (warp < 8) softmax_role<D, SCORE>(p, sh, smem, tmem, warp / 4, x0, x1, wd);
     else if (warp == kLoadWarp) load_role<D>(p, sh, smem, x0, x1, wd);
@@ -526,13 +546,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows;
     const long long T = (long long)p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
     const int entries = one ? (p.geom.pages + 1) / 2 : p.geom.pages;
-    const int c0 = pd_holder(T, start, p.used), c1 = pd_holder(T, start + entries - 1, p.used);
+    wait_prerequisites();
+    const int used = __ldcg(p.split);
+    const int c0 = pd_holder(T, start, used), c1 = pd_holder(T, start + entries - 1, used);
     const int parts = (c1 - c0 + 1) * (one ? 2 : 1);
     const int64_t step = one ? 1 : 2;  // slots from a part to the next
     const int64_t slot0 = 2 * ((int64_t)hk * sp_cols(p.geom) + col + c0) + s0;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot0 * kSpRows + r;
     const float4* po = reinterpret_cast<const float4*>(p.part_o) + (slot0 * (D / 4) + c4) * kSpRows + r;
-    wait_prerequisites();
     const int64_t own = ((int64_t)b * p.Hkv + hk) * p.rows + j;
     float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     if (takes) {
@@ -540,7 +561,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         const float4 x = __ldcg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
         M = last.x;
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[k * step * kSpRows].x);
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(ml + k * step * kSpRows).x);
         const float Mu = M == -INFINITY ? 0.f : M;
         auto take = [&](float2 w, float4 y) {
             const float f = ex2_approx(w.x - Mu);
@@ -551,7 +572,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             L = fmaf(w.y, f, L);
         };
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) take(ml[k * step * kSpRows], __ldcg(po + k * step * (D / 4) * kSpRows));
+        for (int k = 0; k < parts; ++k) take(__ldcg(ml + k * step * kSpRows), __ldcg(po + k * step * (D / 4) * kSpRows));
         take(last, x);
     }
     const bool some = L > 0.f && M != -INFINITY;
@@ -587,7 +608,9 @@ cudaError_t launch_variant(const SpParams& p, cudaStream_t stream)
             if (current_ctx(&key)) done.push_back(key);
         }
     }
-    kern<<<(unsigned)p.used, kSpThreads, SpCfg<D>::SMEM, stream>>>(p);
+    const long long entries = (long long)p.Hkv * p.geom.per_head;
+    const unsigned grid = (unsigned)(entries < p.sms - 1 ? entries : p.sms - 1);  // sp_split's most
+    kern<<<grid, kSpThreads, SpCfg<D>::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 

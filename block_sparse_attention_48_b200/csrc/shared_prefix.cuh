@@ -26,7 +26,8 @@ struct SpParams {
     const float* slopes;
 
     SpGeom geom;
-    int32_t used;    // CTAs, each with a share of the list
+    int32_t sms;     // shared out between the prefix and the sequences' own pages
+    int32_t* split;  // CTAs that took a share of the list, for the join
     // Partial results: of CTA c's piece of column col (counted over the heads) and stream
     // s, slot 2 (col + c) + s
     float* part_o;   // [slot][D / 4][128][4] fp32, unnormalised
@@ -38,7 +39,10 @@ struct SpParams {
     float* lse;            // [B, Hq, q_len] or null
     const float* own_o;    // [B][Hkv][rows][D] fp32, unnormalised
     const float* own_ml;   // [B][Hkv][rows][2]
-    int32_t pt_width;
+
+    // of pd_range
+    int32_t pt_width, prefix_pages, has_window;
+    int64_t window;
 
     int* status;
     uint64_t watchdog_ns;

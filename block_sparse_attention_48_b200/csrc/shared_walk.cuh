@@ -77,4 +77,16 @@ FA_SP_FN int sp_tiles(const SpGeom& g, const SpPiece& p, int s)
 // List position of a column's first entry.
 FA_SP_FN long long sp_start(const SpGeom& g, int hk, int col) { return (long long)hk * g.per_head + (long long)col * g.pages; }
 
+// SMs that take the prefix while the others take the sequences' own pages: in
+// proportion to the two lists' costs (at D = 128, with one CTA per SM: an entry 2.1 us, a
+// page 0.6 us), so that both end together.  The same on every CTA of both kernels.
+FA_SP_FN int sp_split(long long entries, long long own_pages, int sms)
+{
+    const long long a = 7 * entries, b = 2 * own_pages;
+    long long n = a + b > 0 ? (sms * a + (a + b) / 2) / (a + b) : 1;
+    const long long most = entries < sms - 1 ? entries : sms - 1;
+    n = n < most ? n : most;
+    return n < 1 ? 1 : (int)n;
+}
+
 } // namespace fa
