@@ -576,16 +576,20 @@ def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, amplitude: float, devi
 
 _paged_workspaces = {}
 _STATUS_BYTES = int(_lib.fa_workspace_size())
+_ZEROED_BYTES = 1 << 14  # more than the status word and the counters
 
 
 def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
     """The workspace paged_append, flex_decode_paged and flex_decode_shared use by
     default: one per device and stream, zero-filled when allocated; a larger one takes
     over its predecessor's status word (the predecessor is kept alive).  While a CUDA
-    graph is captured each call gets a zero-filled workspace of the graph's own instead
-    (pass ws= to read the status of captured calls)."""
+    graph is captured each call gets a workspace of the graph's own instead (pass ws= to
+    read the status of captured calls), of which every replay zeroes the status word and
+    the counters behind it."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros((max(need, _STATUS_BYTES),), dtype=torch.uint8, device=device)
+        ws = torch.empty((max(need, _ZEROED_BYTES),), dtype=torch.uint8, device=device)
+        ws[:_ZEROED_BYTES].zero_()
+        return ws
     index = device.index if device.index is not None else torch.cuda.current_device()
     kept = _paged_workspaces.setdefault((index, _raw_stream(index)), [])
     if not kept or kept[-1].numel() < need:

@@ -46,6 +46,7 @@ namespace {
 constexpr int kBox = 16384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;  // log2 of the growth that moves the running maximum
 
 template <int D>
 struct PdCfg {
@@ -399,13 +400,13 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     // products; V's tile is waited for when it is needed.
     auto page = [&](uint32_t kbase, uint32_t vbase, int kv0, int pos0, int pos1, bool edge, uint64_t* k_free,
                     uint64_t* v_full, uint32_t v_phase) {
-        float sacc[2][NR][4];
+        float sacc[2][NR][4], sodd[2][NR][4];  // two chains of products for each tile of keys
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[kt][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sacc[kt][nt][e] = sodd[kt][nt][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KD; ++kk)
 #pragma unroll
@@ -413,9 +414,15 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 uint32_t ka[4];
                 ldsm_x4(swz(kbase, key0 + 16 * kt + 8 * (m4 & 1) + (lane & 7), 2 * kk + (m4 >> 1)), ka);
 #pragma unroll
-                for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(sacc[kt][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
+                for (int nt = 0; nt < NR; ++nt)
+                    mma_bf16_16816(kk & 1 ? sodd[kt][nt] : sacc[kt][nt], ka, qb[nt][kk][0], qb[nt][kk][1]);
             }
-
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[kt][nt][e] += sodd[kt][nt][e];
         __syncwarp();
         if (lane == 0) mbar_arrive(k_free);
 
@@ -475,21 +482,40 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                     sacc[kt][nt][e] = x;
                     mt_[nt][j] = fmaxf(mt_[nt][j], x);
                 }
-        float alpha[NR][2], m_use[NR][2];
+        // The running maximum moves only when a score exceeds it by 2^8 (the first score of
+        // all does), so that most pages need neither the reductions nor the rescaling.
+        bool grows = false;
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float m = mt_[nt][j];
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                const float m_new = fmaxf(m_run[nt][j], m);
-                m_use[nt][j] = m_new == -INFINITY ? 0.f : m_new;
-                alpha[nt][j] = ex2_approx(m_run[nt][j] - m_use[nt][j]);  // 0 while nothing was admitted
-                m_run[nt][j] = m_new;
-                l_run[nt][j] *= alpha[nt][j];
-            }
+            for (int j = 0; j < 2; ++j) grows |= mt_[nt][j] > m_run[nt][j] + kRescale;
+        if (__any_sync(0xFFFFFFFFu, grows)) {
+            float alpha[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float m = mt_[nt][j];
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                    m = fmaxf(m_run[nt][j], m);
+                    alpha[nt][j] = ex2_approx(m_run[nt][j] - (m == -INFINITY ? 0.f : m));  // 0 while nothing was admitted
+                    m_run[nt][j] = m;
+                    l_run[nt][j] *= alpha[nt][j];
+                }
+#pragma unroll
+            for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
+        }
+        float m_use[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m_use[nt][j] = m_run[nt][j] == -INFINITY ? 0.f : m_run[nt][j];
         // P^T in bf16 (at most 2^-8 of each entry, as in every kernel here: the tensor
         // core's operand type); the sum is taken of the unrounded values
         uint32_t pb[2][NR][2];
@@ -506,47 +532,29 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                 pb[kt][nt][0] = movmatrix_t(pack_bf16x2(pv[0], pv[1]));  // keys 0-7
                 pb[kt][nt][1] = movmatrix_t(pack_bf16x2(pv[2], pv[3]));  // keys 8-15
             }
-#pragma unroll
-        for (int mt = 0; mt < KD; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) oacc[mt][nt][e] *= alpha[nt][e & 1];
         // after a timeout V's tile may not have landed: whatever it holds
         __all_sync(0xFFFFFFFFu, mbar_wait(v_full, v_phase, wd));
         // V^T of 16 columns (mt) and 16 keys (kt)
         auto load_v = [&](int mt, int kt, uint32_t (&va)[4]) {
             ldsm_x4_trans(swz(vbase, key0 + 16 * kt + 8 * (m4 >> 1) + (lane & 7), 2 * mt + (m4 & 1)), va);
         };
-        if (!edge) {
+        // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the same + 8 that
+        // a row at positions [from, to] may attend
+        auto keep = [&](int kt, int from, int to, uint32_t (&k2)[2]) {
 #pragma unroll
-            for (int mt = 0; mt < KD; ++mt)
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt) {
-                    uint32_t va[4];
-                    load_v(mt, kt, va);
-#pragma unroll
-                    for (int nt = 0; nt < NR; ++nt)
-                        mma_bf16_16816(oacc[mt][nt], va, pb[kt][nt][0], pb[kt][nt][1]);
-                }
-        } else {
-            // register masks of V^T's keys 2 tq, 2 tq + 1 (low, high half) and the
-            // same + 8 that a row at positions [from, to] may attend
-            auto keep = [&](int kt, int from, int to, uint32_t (&k2)[2]) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kv = kv0 + 16 * kt + 2 * tq + 8 * h;
-                    const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
-                    const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
-                    k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
-                }
-            };
-            uint32_t k2[2][2];
+            for (int h = 0; h < 2; ++h) {
+                const int kv = kv0 + 16 * kt + 2 * tq + 8 * h;
+                const bool a = kv <= to && (!p.has_window || (int64_t)from - kv <= p.window);
+                const bool b = kv + 1 <= to && (!p.has_window || (int64_t)from - (kv + 1) <= p.window);
+                k2[h] = (a ? 0x0000FFFFu : 0u) | (b ? 0xFFFF0000u : 0u);
+            }
+        };
+        uint32_t k2[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+        bool odd = false;
+        if (edge) {
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt) keep(kt, pos0, pos1, k2[kt]);
-            // an infinity or NaN that some rows attend and others may not: one product per
-            // token, each with its own keys, kept for its rows only
-            bool odd = false;
+            // an infinity or NaN that some rows attend and others may not
             if (p.q_len > 1) {
 #pragma unroll 1
                 for (int mt = 0; mt < KD; ++mt)
@@ -559,12 +567,27 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                     }
                 odd = __any_sync(0xFFFFFFFFu, odd);
             }
-            const int passes = odd ? p.q_len : 1;
-#pragma unroll 1
-            for (int t = 0; t < passes; ++t) {
-                if (odd)
+        }
+        if (!odd) {
+            // (masked on every page: a second copy of the products for the masked pages alone
+            // took three times as long on them, most of it for fetching the code)
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) keep(kt, pos0 + t, pos0 + t, k2[kt]);
+            for (int mt = 0; mt < KD; ++mt)
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t vr[4];
+                    load_v(mt, kt, vr);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vr[e] &= k2[kt][e >> 1];
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(oacc[mt][nt], vr, pb[kt][nt][0], pb[kt][nt][1]);
+                }
+        } else {
+            // one product per token, each with its own keys, kept for its rows only
+#pragma unroll 1
+            for (int t = 0; t < p.q_len; ++t) {
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) keep(kt, pos0 + t, pos0 + t, k2[kt]);
 #pragma unroll
                 for (int mt = 0; mt < KD; ++mt)
 #pragma unroll
@@ -581,7 +604,7 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
                             mma_bf16_16816(d4, vr, pb[kt][nt][0], pb[kt][nt][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (!odd || tok[nt][e & 1] == t) oacc[mt][nt][e] = d4[e];
+                                if (tok[nt][e & 1] == t) oacc[mt][nt][e] = d4[e];
                         }
                     }
             }
