@@ -270,12 +270,12 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
     if (B * Hq * q_len == 0) return FA_OK;
     if (!seq_lens || (pages_per_seq > 0 && (!page_table || num_pages < 1))) return FA_ERR_INVALID_ARG;
-    // entries of the prefix's list for a head, and its rows
-    if (prefix_pages > 0 && (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
+    // the kernels' work lists
+    if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;
+    if (prefix_pages > 0 && Hkv * (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
         return FA_ERR_UNSUPPORTED;
     const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
     if (lay.sms <= 0) return FA_ERR_CUDA;
-    if (B * Hkv * pages_per_seq > kMaxLen * lay.sms) return FA_ERR_UNSUPPORTED;  // a CTA's pages: int32
     if (workspace_bytes < lay.end) return FA_ERR_INVALID_ARG;
 
     fa::PdParams P;
@@ -336,7 +336,8 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.slopes = P.slopes;
     S.geom = fa::sp_geom(B * P.rows, (int32_t)prefix_pages);
     P.sms = lay.sms;
-    P.prefix_entries = Hkv * S.geom.per_head;
+    P.prefix_entries = (int32_t)Hkv * S.geom.per_head;
+    P.prefix_columns = (int32_t)Hkv * fa::sp_cols(S.geom);
     S.sms = P.sms;
     S.split = reinterpret_cast<int32_t*>(ws + lay.split);
     S.part_ml = reinterpret_cast<float*>(ws + lay.pre_ml);

@@ -61,7 +61,7 @@ struct PdCfg {
 struct __align__(16) PdShared {
     uint64_t full[kPdTeams][6], empty[kPdTeams][6];
     long long scan[kPdThreads / 32];
-    long long total;                          // list length
+    int total;                                // list length
     int used, ctas;                           // teams that have work, and their CTAs
     PdWalk start[kPdTeams];                   // where a team's share starts
     int last[kPdTeams][2];                    // this team completed the split segment
@@ -109,7 +109,7 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
     const int per = (p.B + kPdThreads - 1) / kPdThreads;
     const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
     long long mine = 0;
-    for (int b = lo; b < hi; ++b) mine += pd_range(p, __ldg(p.seq_lens + b), bad).n;
+    for (int b = lo; b < hi; ++b) mine += pd_weight(pd_range(p, __ldg(p.seq_lens + b), bad));
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -123,10 +123,11 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
         before += w < warp ? sh.scan[w] : 0;
         total += sh.scan[w];
     }
-    const long long T = total * p.Hkv;
+    const long long pages = (1ll << kPdCount) - 1;
+    const int T = (int)(total & pages) * p.Hkv;
     // beside a shared prefix, the CTAs that its kernel leaves SMs to
-    const int ctas = p.prefix_entries ? min(p.grid, p.sms - sp_split(p.prefix_entries, T, p.sms)) : p.grid;
-    const int used = (int)min(T, (long long)min(p.teams, ctas * kPdTeams));
+    const int ctas = p.prefix_entries ? min(p.grid, p.sms - sp_split(p.prefix_entries, p.prefix_columns, T, (int)(total >> kPdCount) * p.Hkv, p.sms)) : p.grid;
+    const int used = min(T, min(p.teams, ctas * kPdTeams));
     if (tid == 0) {
         sh.total = T;
         sh.used = used;
@@ -135,9 +136,9 @@ __device__ __forceinline__ void pd_locate(const PdParams& p, PdShared& sh, bool&
 #pragma unroll
     for (int team = 0; team < kPdTeams; ++team) {
         if (pd_team(ctas, team) >= used) continue;
-        const long long x0 = pd_share(T, pd_team(ctas, team), used);
-        const long long acc = before + inc - mine;  // pages of the sequences before this thread's
-        if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + mine)) pd_find(p, x0, lo, hi, acc, sh.start[team], bad);
+        const int x0 = pd_share(T, pd_team(ctas, team), used);
+        const int acc = (int)((before + inc - mine) & pages);  // of the sequences before this thread's
+        if (p.Hkv * acc <= x0 && x0 < p.Hkv * (acc + (int)(mine & pages))) pd_find(p, x0, lo, hi, acc, sh.start[team], bad);
     }
     __syncthreads();
 }
@@ -171,11 +172,11 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     const int me = pd_team(sh.ctas, team);
     uint64_t *full = sh.full[team], *empty = sh.empty[team];
     uint8_t* ring = smem + team * C::NT * C::TILE;
-    const long long T = sh.total;
+    const int T = sh.total;
     const int used = sh.used;
     const bool works = me < used;
-    const long long x0 = works ? pd_share(T, me, used) : 0;
-    const int count = works ? (int)(pd_share(T, me + 1, used) - x0) : 0;
+    const int x0 = works ? pd_share(T, me, used) : 0;
+    const int count = works ? pd_share(T, me + 1, used) - x0 : 0;
     PdWalk w{0, 0, 0, {0, 0, 0, 0}};
     if (works) w = sh.start[team];
 
@@ -614,9 +615,9 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     // the share's first and last piece where they are parts of a split segment, and the
     // list positions of those segments
     PdWalk head = w, tail = w;
-    long long xhead = -1, xtail = -1;
+    int xhead = -1, xtail = -1;
     if (count > 0) load_segment(w.b, w.hk);
-    long long xseg = x0 - w.t;  // list position of the segment's first page
+    int xseg = x0 - w.t;  // list position of the segment's first page
     uint32_t slot = 0, phase = 0;  // of the next tile
     auto step = [&]() {
         if (++slot == C::NT) {

@@ -41,7 +41,7 @@ struct PdParams {
     // c0's share) and 2 c for c in (c0, c1] (the start of c's share)
     int32_t grid, teams;  // CTAs, and at most kPdTeams of each
     int32_t sms;                // with a shared prefix: the SMs, of which sp_split leaves some
-    int64_t prefix_entries;     // to the prefix and its list of so many entries
+    int32_t prefix_entries, prefix_columns;  // to the prefix and its list
     float* part_o;        // [2 * teams][rows][D] fp32, unnormalised
     float* part_ml;       // [2 * teams][rows][2]: running max (log2 units), sum
     unsigned* arrived;    // [teams] pieces done of the segment whose first piece ends share c0;

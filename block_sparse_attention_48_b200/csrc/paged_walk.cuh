@@ -32,17 +32,33 @@ __device__ __forceinline__ PdRange pd_range(const P& p, int32_t raw_len, bool& b
     return r;
 }
 
-// CTA c of the `used` CTAs that have work takes list entries
-// [pd_share(T, c, used), pd_share(T, c + 1, used)); used <= T, so no share is empty.
-__device__ __forceinline__ long long pd_share(long long T, int c, int used)
+// A sequence's pages and, above kPdCount, whether it has any: sums of these hold both the
+// pages (below 2^31) and the sequences.
+constexpr int kPdCount = 44;
+
+__device__ __forceinline__ long long pd_weight(const PdRange& r)
 {
-    return (T / used) * c + (T % used) * c / used;
+    return r.n > 0 ? r.n + (1ll << kPdCount) : 0;
 }
 
-// The CTA that holds list entry x.
-__device__ __forceinline__ int pd_holder(long long T, long long x, int used)
+// Worker c of the `used` workers that have work takes list entries
+// [pd_share(T, c, used), pd_share(T, c + 1, used)), floor(c T / used) and on; used <= T, so
+// no share is empty, and T < 2^31.  (Divisions of 64 bits would be most of the code that a
+// CTA fetches before it can start.)
+__device__ __forceinline__ int pd_share(int T, int c, int used)
 {
-    return (int)(((x + 1) * used - 1) / T);
+    const uint32_t t = T, u = used;
+    return (int)(t / u * c + t % u * c / u);
+}
+
+// The worker that holds list entry x: an estimate, off by one at most, put right.
+__device__ __forceinline__ int pd_holder(int T, int x, int used)
+{
+    int c = (int)(((float)x + 1.f) * ((float)used / (float)T));
+    c = c < used ? c : used - 1;
+    while (pd_share(T, c, used) > x) --c;
+    while (pd_share(T, c + 1, used) <= x) ++c;
+    return c;
 }
 
 // A position in the work list: page t of the range of segment (b, hk).
@@ -54,14 +70,13 @@ struct PdWalk {
 // Position x0 of the list, given that it lies in the segments of sequences [lo, hi)
 // and that the sequences before lo have `before` pages a kv head.
 template <class P>
-__device__ __forceinline__ bool pd_find(const P& p, long long x0, int lo, int hi, long long before, PdWalk& w,
-                                        bool& bad)
+__device__ __forceinline__ bool pd_find(const P& p, int x0, int lo, int hi, int before, PdWalk& w, bool& bad)
 {
     for (int b = lo; b < hi; ++b) {
         const PdRange r = pd_range(p, __ldg(p.seq_lens + b), bad);
         if (x0 < p.Hkv * (before + r.n)) {
-            const long long off = x0 - p.Hkv * before;
-            w = PdWalk{b, (int)(off / r.n), (int)(off % r.n), r};
+            const int off = x0 - p.Hkv * before;
+            w = PdWalk{b, off / r.n, off % r.n, r};
             return true;
         }
         before += r.n;

@@ -82,7 +82,7 @@ __device__ __forceinline__ SpSeq entry_seq(const SpGeom& g, const SpPiece& p, in
 }
 
 template <int D>
-__device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8_t* smem, long long x0, long long x1,
+__device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8_t* smem, int x0, int x1,
                                           Watchdog& wd)
 {
     using C = SpCfg<D>;
@@ -112,7 +112,7 @@ __device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8
         }
         return pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, t & 31), p.num_pages, bad);
     };
-    for (long long x = x0; ok && x < x1;) {
+    for (int x = x0; ok && x < x1;) {
         const SpPiece pc = sp_piece(p.geom, x, x1);
         for (int e = pc.e0; ok && e < pc.e0 + pc.n; ++e) {
             if (!pc.one) {
@@ -144,8 +144,8 @@ __device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8
 __device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) { return ((uint64_t)hi << 32) | lo; }
 
 template <int D, int s>
-__device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_t* smem, uint32_t tmem, long long x0,
-                                         long long x1, Watchdog& wd)
+__device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_t* smem, uint32_t tmem, int x0,
+                                         int x1, Watchdog& wd)
 {
     using C = SpCfg<D>;
     const uint32_t hi_k = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
@@ -199,7 +199,7 @@ __device__ __forceinline__ void mma_role(const SpParams& p, SpShared& sh, uint8_
         }
         __syncwarp();
     };
-    for (long long x = x0; ok && x < x1;) {
+    for (int x = x0; ok && x < x1;) {
         const SpPiece pc = sp_piece(p.geom, x, x1);
         const int n = sp_tiles(p.geom, pc, s);
         if (n > 0) {
@@ -287,7 +287,7 @@ __device__ __forceinline__ float max_row(const float (&x)[64])
 
 template <int D, int SCORE>
 __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, uint8_t* smem, uint32_t tmem, int s,
-                                             long long x0, long long x1, Watchdog& wd)
+                                             int x0, int x1, Watchdog& wd)
 {
     using C = SpCfg<D>;
     constexpr int U = D / 8;  // 16-byte units of a row
@@ -298,7 +298,7 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
     uint32_t tile = 0, piece = 0;
     const float F = SCORE == FA_SCORE_SOFTCAP ? p.softcap * kLog2e : SCORE == FA_SCORE_ALIBI ? 1.f : p.scale * kLog2e;
     bool ok = true;
-    for (long long x0p = x0; ok && x0p < x1;) {
+    for (int x0p = x0; ok && x0p < x1;) {
         const SpPiece pc = sp_piece(p.geom, x0p, x1);
         const int n = sp_tiles(p.geom, pc, s);
         const long long col = (long long)pc.hk * sp_cols(p.geom) + pc.col;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     long long own = 0;
     {
         bool bad = false;
-        for (int b = threadIdx.x; b < p.B; b += kSpThreads) own += pd_range(p, __ldg(p.seq_lens + b), bad).n;
+        for (int b = threadIdx.x; b < p.B; b += kSpThreads) own += pd_weight(pd_range(p, __ldg(p.seq_lens + b), bad));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xFFFFFFFFu, own, o);
         if (threadIdx.x % 32 == 0) sh.pages[warp] = own;
@@ -500,15 +500,15 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    const long long T = (long long)p.Hkv * p.geom.per_head;
+    const int T = p.Hkv * p.geom.per_head;
     own = 0;
 #pragma unroll
     for (int w = 0; w < kSpThreads / 32; ++w) own += sh.pages[w];
-    const int used = sp_split(T, own * p.Hkv, p.sms);
+    const int used = sp_split(T, p.Hkv * sp_cols(p.geom), (int)(own & ((1ll << kPdCount) - 1)) * p.Hkv,
+                              (int)(own >> kPdCount) * p.Hkv, p.sms);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.split = used;
     const bool works = (int)blockIdx.x < used;
-    const long long x0 = works ? pd_share(T, blockIdx.x, used) : 0;
-    const long long x1 = works ? pd_share(T, blockIdx.x + 1, used) : 0;
+    const int x0 = works ? pd_share(T, blockIdx.x, used) : 0, x1 = works ? pd_share(T, blockIdx.x + 1, used) : 0;
     Watchdog wd{p.watchdog_ns, false};
     if (warp < 8) softmax_role<D, SCORE>(p, sh, smem, tmem, warp / 4, x0, x1, wd);
     else if (warp == kLoadWarp) load_role<D>(p, sh, smem, x0, x1, wd);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int col = R / (2 * kSpRows), r = R % kSpRows;  // the same column and tile in all lanes
     const bool one = col >= p.geom.pairs;
     const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows;
-    const long long T = (long long)p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
+    const int T = p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
     const int entries = one ? (p.geom.pages + 1) / 2 : p.geom.pages;
     wait_prerequisites();
     const int used = __ldcg(p.split);

@@ -30,7 +30,7 @@ struct SpGeom {
 #define FA_SP_FN inline
 #endif
 
-// The caller bounds R and pages so that per_head fits 32 bits.
+// The caller bounds R and pages so that the list of all heads is below 2^31.
 FA_SP_FN SpGeom sp_geom(int64_t R, int32_t pages)
 {
     SpGeom g;
@@ -53,17 +53,17 @@ struct SpPiece {
 };
 
 // The piece at list position x of a share that ends at x1 (x < x1).
-FA_SP_FN SpPiece sp_piece(const SpGeom& g, long long x, long long x1)
+FA_SP_FN SpPiece sp_piece(const SpGeom& g, int x, int x1)
 {
     SpPiece p;
-    p.hk = (int)(x / g.per_head);
-    const int off = (int)(x % g.per_head);
+    p.hk = x / g.per_head;
+    const int off = x % g.per_head;
     const int paired = g.pairs * g.pages;
     p.one = off >= paired;
     p.col = p.one ? g.pairs : off / g.pages;
     p.e0 = off - p.col * g.pages;
     const int left = (p.one ? (g.pages + 1) / 2 : g.pages) - p.e0;
-    p.n = left < x1 - x ? left : (int)(x1 - x);
+    p.n = left < x1 - x ? left : x1 - x;
     return p;
 }
 
@@ -75,18 +75,24 @@ FA_SP_FN int sp_tiles(const SpGeom& g, const SpPiece& p, int s)
 }
 
 // List position of a column's first entry.
-FA_SP_FN long long sp_start(const SpGeom& g, int hk, int col) { return (long long)hk * g.per_head + (long long)col * g.pages; }
+FA_SP_FN int sp_start(const SpGeom& g, int hk, int col) { return hk * g.per_head + col * g.pages; }
 
 // SMs that take the prefix while the others take the sequences' own pages: in
-// proportion to the two lists' costs (at D = 128, with one CTA per SM: an entry 2.1 us, a
-// page 0.6 us), so that both end together.  The same on every CTA of both kernels.
-FA_SP_FN int sp_split(long long entries, long long own_pages, int sms)
+// proportion to the two lists' costs, so that both end together, and if that is near a
+// multiple of the columns, that multiple: no share then runs over two columns, whose end
+// and start cost a CTA as much as four entries.  The same on every CTA of both kernels.
+// In tenths of a microsecond of an SM: an entry 16, a page 5, and 10 for a segment's start
+// and end.
+FA_SP_FN int sp_split(int entries, int columns, int own_pages, int own_segments, int sms)
 {
-    const long long a = 7 * entries, b = 2 * own_pages;
-    long long n = a + b > 0 ? (sms * a + (a + b) / 2) / (a + b) : 1;
-    const long long most = entries < sms - 1 ? entries : sms - 1;
+    const float a = 16.f * entries, b = 5.f * own_pages + 10.f * own_segments;
+    const int most = entries < sms - 1 ? entries : sms - 1;
+    int n = a > 0.f ? (int)(sms * (a / (a + b)) + 0.5f) : 1;
     n = n < most ? n : most;
-    return n < 1 ? 1 : (int)n;
+    n = n < 1 ? 1 : n;
+    int m = (n + columns / 2) / columns * columns;
+    if (m > most) m -= columns;
+    return m > 0 && 8 * (m > n ? m - n : n - m) <= n ? m : n;
 }
 
 } // namespace fa

@@ -446,7 +446,7 @@ size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_
  *      nothing (a sequence of length 0, or a query token before its first key) gets
  *      O = 0, LSE = -inf.  The same inputs give the same bits.
  * Errors: as fa_decode; FA_ERR_UNSUPPORTED for more than 16 rows per kv head, a bias
- * score_mod or D.  A length below zero or beyond pages_per_seq pages and a page outside
+ * score_mod or D, or B * Hkv * pages_per_seq of 2^31 - 256 and more.  A length below zero or beyond pages_per_seq pages and a page outside
  * the pool are clamped (no read outside the pools) and reported as FA_ERR_BAD_BLOCKMASK
  * by fa_get_device_status. */
 int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
