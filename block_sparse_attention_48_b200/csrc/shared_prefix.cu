@@ -343,12 +343,18 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
             pos = __ldg(p.seq_lens + b) - p.q_len + qi;
         }
         float m_run = -INFINITY, l_run = 0.f;
+        // a warp without rows only passes the barriers on (its rows of P and O are nobody's)
+        const bool rows = __any_sync(0xFFFFFFFFu, valid);
         for (int i = 0; ok && i < n; ++i, ++tile) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const uint32_t s_addr = tmem + C::s_col(s, h) + lanes;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full[s][h], tile & 1, wd));
                 if (!ok) break;
+                if (!rows) {
+                    mbar_arrive_warp(&sh.p_full[s][h]);
+                    continue;
+                }
                 tc_fence_after();
                 float x[64];
                 {
@@ -436,7 +442,7 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
         if (!ok) break;
         ++piece;
         tc_fence_after();
-        *ml = make_float2(m_run, l_run);
+        if (valid) *ml = make_float2(m_run, l_run);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
@@ -447,7 +453,7 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
                 mbar_arrive_warp(&sh.o_empty[s]);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < 8 && valid; ++u)
                 dst[(8 * c + u) * kSpRows] = make_float4(__uint_as_float(ov[4 * u]), __uint_as_float(ov[4 * u + 1]),
                                                          __uint_as_float(ov[4 * u + 2]), __uint_as_float(ov[4 * u + 3]));
         }
