@@ -307,9 +307,8 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
         P.softcap_in = P.scale / sm->softcap;
     }
     P.slopes = kind == FA_SCORE_ALIBI ? sm->alibi_slopes : nullptr;
-    const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more teams than pages in all
+    const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more than pages in all
     P.grid = (int32_t)(most < 1 ? 1 : most < lay.sms ? most : lay.sms);
-    P.teams = (int32_t)(most < 1 ? 1 : most < P.grid * fa::kPdTeams ? most : P.grid * fa::kPdTeams);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     P.part_ml = reinterpret_cast<float*>(ws + lay.ml);
@@ -335,10 +334,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.scale = P.scale; S.softcap = P.softcap; S.softcap_in = P.softcap_in;
     S.slopes = P.slopes;
     S.geom = fa::sp_geom(B * P.rows, (int32_t)prefix_pages);
-    P.sms = lay.sms;
-    P.prefix_entries = (int32_t)Hkv * S.geom.per_head;
-    P.prefix_columns = (int32_t)Hkv * fa::sp_cols(S.geom);
-    S.sms = P.sms;
+    S.sms = lay.sms;
     S.split = reinterpret_cast<int32_t*>(ws + lay.split);
     S.part_ml = reinterpret_cast<float*>(ws + lay.pre_ml);
     S.part_o = reinterpret_cast<float*>(ws + lay.pre_o);
@@ -348,11 +344,9 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.own_o = P.own_o;
     S.own_ml = P.own_ml;
     S.pt_width = P.pt_width;
-    S.prefix_pages = P.prefix_pages;
     S.status = P.status;
     S.watchdog_ns = P.watchdog_ns;
-    if (fa::launch_shared_prefix(S, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
-    if (fa::launch_paged_decode(P, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
+    if (fa::launch_shared_decode(S, P, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
     return fa::launch_shared_join(S, (int)D, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

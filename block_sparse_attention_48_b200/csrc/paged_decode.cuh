@@ -36,15 +36,13 @@ struct PdParams {
     float softcap, softcap_in;
     const float* slopes;
 
-    // Work split: team c of `teams` takes the c-th share of the list of pages.  A segment
+    // Work split: team c of those that have work takes the c-th share of the list of pages.  A segment
     // split over teams c0..c1 leaves partial results 2 c0 + 1 (its first piece, the end of
     // c0's share) and 2 c for c in (c0, c1] (the start of c's share)
-    int32_t grid, teams;  // CTAs, and at most kPdTeams of each
-    int32_t sms;                // with a shared prefix: the SMs, of which sp_split leaves some
-    int32_t prefix_entries, prefix_columns;  // to the prefix and its list
+    int32_t grid;         // CTAs, of kPdTeams teams each
     float* part_o;        // [2 * teams][rows][D] fp32, unnormalised
     float* part_ml;       // [2 * teams][rows][2]: running max (log2 units), sum
-    unsigned* arrived;    // [teams] pieces done of the segment whose first piece ends share c0;
+    unsigned* arrived;    // [team] pieces done of the segment whose first piece ends share c0;
                           // every call leaves zeros
 
     // With a shared prefix: the state (log2 max, sum, unnormalised O) of the rows whose

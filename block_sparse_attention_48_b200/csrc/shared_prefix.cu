@@ -1,6 +1,6 @@
 // Decoding behind a shared prefix for sm_100a: the attention of every sequence's query
-// rows to the keys that all of them share, taken as one matrix problem per kv head, and
-// its join with the sequences' own parts (paged_decode.cu).
+// rows to the keys that all of them share, taken as one matrix problem per kv head,
+// beside the sequences' own parts (paged_decode_impl.cuh), and the join of both.
 //
 //   rows r = (b, h in group, i) of a kv head, R = B G q_len of them;
 //   S = mod(Q K^T scale) over the prefix, m = row max, l = sum 2^(S - m),
@@ -28,10 +28,7 @@
 
 #include "context.cuh"
 #include "dependent_launch.cuh"
-#include "flex_fwd.cuh"
-#include "flexattn.h"
-#include "ptx.cuh"
-#include "score_math.cuh"
+#include "paged_decode_impl.cuh"
 #include "shared_prefix.cuh"
 
 namespace fa {
@@ -56,11 +53,16 @@ struct SpCfg {
     static constexpr uint32_t o_col(int s) { return 256u + 128u * s; }
 };
 
+// Of the kernel, whose CTAs do one or the other.
+template <int D>
+struct SharedSmem {
+    static constexpr int BYTES = SpCfg<D>::SMEM > pd::Cfg<D>::SMEM ? SpCfg<D>::SMEM : pd::Cfg<D>::SMEM;
+};
+
 struct __align__(16) SpShared {
     uint64_t full[12], empty[12];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem_base;
-    long long pages[kSpThreads / 32];  // of the sequences' own, by warp
 };
 
 // Ring positions of an entry's tiles for a stream: K at `k`, V at `v`.
@@ -461,25 +463,12 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
     if (wd.failed && lane == 0) atomicOr(p.status, STATUS_TIMEOUT);
 }
 
+// CTA `block` of `ctas` that take the prefix.
 template <int D, int SCORE>
-__global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __grid_constant__ SpParams p)
+__device__ __forceinline__ void prefix_cta(const SpParams& p, SpShared& sh, uint8_t* smem, int block, int ctas)
 {
     using C = SpCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ SpShared sh;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x / 32;
-    launch_dependents();
-    // the sequences' own pages, which decide how many SMs the prefix gets (a bad length is
-    // reported by the paged decode)
-    long long own = 0;
-    {
-        bool bad = false;
-        for (int b = threadIdx.x; b < p.B; b += kSpThreads) own += pd_weight(pd_range(p, __ldg(p.seq_lens + b), bad));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xFFFFFFFFu, own, o);
-        if (threadIdx.x % 32 == 0) sh.pages[warp] = own;
-    }
     if (warp == kMmaWarp) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
@@ -506,15 +495,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    const int T = p.Hkv * p.geom.per_head;
-    own = 0;
-#pragma unroll
-    for (int w = 0; w < kSpThreads / 32; ++w) own += sh.pages[w];
-    const int used = sp_split(T, p.Hkv * sp_cols(p.geom), (int)(own & ((1ll << kPdCount) - 1)) * p.Hkv,
-                              (int)(own >> kPdCount) * p.Hkv, p.sms);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.split = used;
-    const bool works = (int)blockIdx.x < used;
-    const int x0 = works ? pd_share(T, blockIdx.x, used) : 0, x1 = works ? pd_share(T, blockIdx.x + 1, used) : 0;
+    const int T = p.Hkv * p.geom.per_head, x0 = pd_share(T, block, ctas), x1 = pd_share(T, block + 1, ctas);
     Watchdog wd{p.watchdog_ns, false};
     if (warp < 8) softmax_role<D, SCORE>(p, sh, smem, tmem, warp / 4, x0, x1, wd);
     else if (warp == kLoadWarp) load_role<D>(p, sh, smem, x0, x1, wd);
@@ -525,6 +506,36 @@ __global__ void __launch_bounds__(kSpThreads, 1) shared_prefix_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// The first CTAs take the prefix, the others the sequences' own pages; how many each from
+// the lengths, on every CTA alike.
+template <int D, int SCORE, int NR>
+__global__ void __launch_bounds__(kSpThreads, 1)
+shared_decode_kernel(const __grid_constant__ SpParams p, const __grid_constant__ PdParams own)
+{
+    extern __shared__ uint8_t smem_raw[];
+    union State {
+        SpShared sp;
+        pd::Shared pd;
+    };
+    __shared__ __align__(16) uint8_t state[sizeof(State)];
+    __shared__ long long scratch[kSpThreads / 32];
+    static_assert(SharedSmem<D>::BYTES + sizeof(state) + sizeof(scratch) <= 227 * 1024,
+                  "shared memory beyond 227 KB per CTA");
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    launch_dependents();
+    bool bad = false;
+    const pd::Scan scan = pd::scan_lengths<kSpThreads>(own, scratch, bad);
+    const int ctas = sp_split(p.Hkv * p.geom.per_head, p.Hkv * sp_cols(p.geom), pd::Scan::pages(scan.total) * p.Hkv,
+                              pd::Scan::sequences(scan.total) * p.Hkv, gridDim.x);
+    if ((int)blockIdx.x < ctas) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.split = ctas;
+        prefix_cta<D, SCORE>(p, reinterpret_cast<State*>(state)->sp, smem, blockIdx.x, ctas);
+    } else {
+        pd::decode_cta<D, SCORE, NR, kSpThreads>(own, reinterpret_cast<State*>(state)->pd, smem, blockIdx.x - ctas,
+                                                 gridDim.x - ctas, scan, bad);
+    }
 }
 
 // The join: a lane a row and a warp four columns of 32, so that the partial results are
@@ -596,12 +607,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         *reinterpret_cast<uint2*>(p.o + where[row] + blockIdx.z * kJoinCols + 4 * u) = out[row][u];
 }
 
-template <int D, int SCORE>
-cudaError_t launch_variant(const SpParams& p, cudaStream_t stream)
+template <int D, int SCORE, int NR>
+cudaError_t launch_variant(const SpParams& p, const PdParams& own, cudaStream_t stream)
 {
     static std::mutex mu;
     static std::vector<CtxKey> done;
-    auto kern = shared_prefix_kernel<D, SCORE>;
+    auto kern = shared_decode_kernel<D, SCORE, NR>;
     {
         CtxKey key;
         std::lock_guard<std::mutex> lock(mu);
@@ -609,23 +620,22 @@ cudaError_t launch_variant(const SpParams& p, cudaStream_t stream)
         if (current_ctx(&key))
             for (const CtxKey& k : done) have |= k == key;
         if (!have) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SpCfg<D>::SMEM);
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedSmem<D>::BYTES);
             if (e != cudaSuccess) return e;
             if (current_ctx(&key)) done.push_back(key);
         }
     }
-    const long long entries = (long long)p.Hkv * p.geom.per_head;
-    const unsigned grid = (unsigned)(entries < p.sms - 1 ? entries : p.sms - 1);  // sp_split's most
-    kern<<<grid, kSpThreads, SpCfg<D>::SMEM, stream>>>(p);
+    kern<<<(unsigned)p.sms, kSpThreads, SharedSmem<D>::BYTES, stream>>>(p, own);
     return cudaGetLastError();
 }
 
 } // namespace
 
-cudaError_t launch_shared_prefix(const SpParams& p, int D, int score_kind, cudaStream_t stream)
+cudaError_t launch_shared_decode(const SpParams& p, const PdParams& own, int D, int score_kind, cudaStream_t stream)
 {
-#define FA_SP_CASE(DD, SS) \
-    if (D == DD && score_kind == SS) return launch_variant<DD, SS>(p, stream);
+#define FA_SP_CASE(DD, SS)                                                               \
+    if (D == DD && score_kind == SS)                                                     \
+        return p.rows > 8 ? launch_variant<DD, SS, 2>(p, own, stream) : launch_variant<DD, SS, 1>(p, own, stream);
     FA_SP_CASE(64, FA_SCORE_NONE) FA_SP_CASE(64, FA_SCORE_ALIBI) FA_SP_CASE(64, FA_SCORE_SOFTCAP)
     FA_SP_CASE(128, FA_SCORE_NONE) FA_SP_CASE(128, FA_SCORE_ALIBI) FA_SP_CASE(128, FA_SCORE_SOFTCAP)
 #undef FA_SP_CASE

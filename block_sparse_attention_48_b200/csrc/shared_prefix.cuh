@@ -1,11 +1,12 @@
-// Launch interface of the shared prefix's attention and of the join with the
-// sequences' own parts.
+// Launch interface of decoding behind a shared prefix: the prefix and the sequences' own
+// parts in one kernel, and their join.
 #pragma once
 
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "paged_decode.cuh"
 #include "shared_walk.cuh"
 
 namespace fa {
@@ -39,16 +40,13 @@ struct SpParams {
     float* lse;            // [B, Hq, q_len] or null
     const float* own_o;    // [B][Hkv][rows][D] fp32, unnormalised
     const float* own_ml;   // [B][Hkv][rows][2]
-
-    // of pd_range
-    int32_t pt_width, prefix_pages, has_window;
-    int64_t window;
+    int32_t pt_width;
 
     int* status;
     uint64_t watchdog_ns;
 };
 
-cudaError_t launch_shared_prefix(const SpParams& p, int D, int score_kind, cudaStream_t stream);
+cudaError_t launch_shared_decode(const SpParams& p, const PdParams& own, int D, int score_kind, cudaStream_t stream);
 cudaError_t launch_shared_join(const SpParams& p, int D, cudaStream_t stream);
 
 } // namespace fa
