@@ -725,9 +725,9 @@ def _decode_pages(name, fn, need, q, k_pages, v_pages, page_table, seq_lens, ext
     q = _readable(q)
     B, Hq, n, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, n, D), dtype=torch.bfloat16, device=device)
+        out = q.new_empty((B, Hq, n, D))
     if lse is None:
-        lse = torch.empty((B, Hq, n), dtype=torch.float32, device=device)
+        lse = q.new_empty((B, Hq, n), dtype=torch.float32)
     elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (B, Hq, n) or not lse.is_contiguous():
         raise TypeError(f"lse: expected a contiguous fp32 tensor [B, Hq, q_len] on {device}")
     qd, od = _desc(q, device, "q"), _desc(out, device, "out")

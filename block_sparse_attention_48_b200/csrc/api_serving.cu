@@ -245,6 +245,16 @@ PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t pref
     return L;
 }
 
+// Whether a shared prefix is taken once, by the kernel made for it, or page by page for
+// every sequence.  The first costs some 15 us more before it reads anything; the second
+// reads (B - 1) Hkv prefix_pages pages again, most of them from L2.  Once / page by page, us
+// on a B200 with cold caches: 33.9 / 25.8 at 2816 such pages (B12 Hkv8 G4 D128, 4096 keys),
+// 34.2 / 38.6 at 5888 (B24), 30.1 / 30.5 at 6016 (B48 Hkv4 G4 D64), 37.6 / 63.3 at 12032 (B48).
+bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t prefix_pages)
+{
+    return (B - 1) * Hkv * prefix_pages >= 6144;
+}
+
 // fa_decode_paged and fa_decode_shared (prefix_len > 0).
 int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
                  int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
@@ -274,6 +284,8 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;
     if (prefix_pages > 0 && Hkv * (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
         return FA_ERR_UNSUPPORTED;
+    const int64_t row0_pages = takes_prefix_once(B, Hkv, prefix_pages) ? 0 : prefix_pages;
+    if (row0_pages) prefix_pages = 0;
     const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
     if (lay.sms <= 0) return FA_ERR_CUDA;
     if (workspace_bytes < lay.end) return FA_ERR_INVALID_ARG;
@@ -299,6 +311,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.pt_width = (int32_t)pages_per_seq;
     P.num_pages = (int32_t)num_pages;
     P.prefix_pages = (int32_t)prefix_pages;
+    P.row0_pages = (int32_t)row0_pages;
     P.has_window = window >= 0 ? 1 : 0;
     P.window = window >= 0 ? (window < kMaxLen ? window : kMaxLen) : 0;
     P.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
@@ -375,7 +388,8 @@ size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64
 {
     if (prefix_len < 0 || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
-    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_len / FA_BLOCK_SIZE).end;
+    const int64_t pages = prefix_len / FA_BLOCK_SIZE;
+    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, pages) ? pages : 0).end;
 }
 
 int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,

@@ -28,7 +28,9 @@ struct PdParams {
     const int32_t* page_table;  // row b at b * pt_stride, pt_width entries
     int64_t pt_stride;
     int32_t pt_width, num_pages;
-    int32_t prefix_pages;       // leading table entries that the sequences share; 0: none
+    int32_t prefix_pages;       // leading table entries whose keys are taken elsewhere; 0: none
+    int32_t row0_pages;         // leading table entries that sequences reaching past them
+                                // read from row 0 (a shared prefix taken page by page)
     int32_t has_window;
     int64_t window;
 

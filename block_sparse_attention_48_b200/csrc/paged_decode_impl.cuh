@@ -178,7 +178,8 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
             if (chunk != (w.t & ~31)) {
                 chunk = w.t & ~31;
                 const int tt = chunk + lane;
-                page_lane = tt < w.r.n ? __ldg(p.page_table + (int64_t)w.b * p.pt_stride + w.r.lo + tt) : 0;
+                const int row = w.r.lo + tt < p.row0_pages && w.r.len - p.q_len >= 128 * p.row0_pages ? 0 : w.b;
+                page_lane = tt < w.r.n ? __ldg(p.page_table + row * p.pt_stride + w.r.lo + tt) : 0;
             }
             const int page = pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, w.t & 31), p.num_pages, bad);
             load(&p.tm_k, w.hk, page);
@@ -349,22 +350,20 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
             const int r = it / (D / 4), d = (it % (D / 4)) * 4;
             const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + r;
             const float* po = p.part_o + (int64_t)r * D + d;
-            float M = -INFINITY;
-#pragma unroll 2
-            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(ml + (2 * (int64_t)c + (c == c0)) * p.rows).x);
-            const float Mu = M == -INFINITY ? 0.f : M;
-            float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+            float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4  // the parts' loads do not wait for one another
             for (int c = c0; c <= c1; ++c) {
                 const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows;
                 const float2 w = __ldcg(ml + part);
                 const float4 x = __ldcg(reinterpret_cast<const float4*>(po + part * D));
-                const float f = ex2_approx(w.x - Mu);
-                L = fmaf(w.y, f, L);
-                v[0] = fmaf(x.x, f, v[0]);
-                v[1] = fmaf(x.y, f, v[1]);
-                v[2] = fmaf(x.z, f, v[2]);
-                v[3] = fmaf(x.w, f, v[3]);
+                const float m = fmaxf(M, w.x), Mu = m == -INFINITY ? 0.f : m;
+                const float f0 = ex2_approx(M - Mu), f = ex2_approx(w.x - Mu);
+                M = m;
+                L = fmaf(w.y, f, L * f0);
+                v[0] = fmaf(x.x, f, v[0] * f0);
+                v[1] = fmaf(x.y, f, v[1] * f0);
+                v[2] = fmaf(x.z, f, v[2] * f0);
+                v[3] = fmaf(x.w, f, v[3] * f0);
             }
             write_out(at.b, at.hk, r, d, at.r.shared, M, L, v);
         }

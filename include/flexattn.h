@@ -419,9 +419,9 @@ int fa_paged_append(const fa_tensor* k, const fa_tensor* v, const fa_tensor* q, 
                     const fa_tensor* v_pages, const fa_tensor* q_out, void* workspace, size_t workspace_bytes,
                     void* stream);
 
-/* Bytes of device workspace fa_decode_paged needs (status word, a counter and two
- * partial results per SM).  Does not depend on the batch or the cache's length, but on
- * the SM count of the current device. */
+/* Bytes of device workspace fa_decode_paged needs (status word; counters and partial
+ * results for every SM).  Does not depend on the batch or the cache's length, but on the
+ * SM count of the current device. */
 size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D);
 
 /* FlexDecoding over a paged cache: the forward pass for a few query tokens per
@@ -439,29 +439,32 @@ size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_
  *      not reach the row.
  *      window < 0: none.  sm: NONE, ALIBI or SOFTCAP (NULL = none); ALiBi's distance is
  *      that of the positions.  scale as fa_forward.
- *      workspace: >= fa_decode_paged_workspace_size(...) bytes, 16-byte aligned, zeroed
- *      once before its first use; every call leaves it ready for the next, of any
- *      shape.  Calls that overlap in time need distinct workspaces.
+ *      workspace: >= fa_decode_paged_workspace_size(...) bytes, 16-byte aligned, its
+ *      first 16 KB zeroed once before its first use; every call leaves it ready for the
+ *      next, of any shape.  Calls that overlap in time need distinct workspaces.
  * Out: o [B, Hq, q_len, D] bf16, lse fp32 [B, Hq, q_len] or NULL; a row that attends
  *      nothing (a sequence of length 0, or a query token before its first key) gets
  *      O = 0, LSE = -inf.  The same inputs give the same bits.
  * Errors: as fa_decode; FA_ERR_UNSUPPORTED for more than 16 rows per kv head, a bias
- * score_mod or D, or B * Hkv * pages_per_seq of 2^31 - 256 and more.  A length below zero or beyond pages_per_seq pages and a page outside
- * the pool are clamped (no read outside the pools) and reported as FA_ERR_BAD_BLOCKMASK
- * by fa_get_device_status. */
+ * score_mod or D, or B * Hkv * pages_per_seq of 2^31 - 256 and more.  A length below zero
+ * or beyond pages_per_seq pages and a page outside the pool are clamped (no read outside
+ * the pools) and reported as FA_ERR_BAD_BLOCKMASK by fa_get_device_status. */
 int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
                     int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
                     const fa_score_mod* sm, float scale, const fa_tensor* o, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace fa_decode_shared needs. */
+/* Bytes of device workspace fa_decode_shared needs; where the prefix is taken once, it
+ * grows with B * Hq * q_len (a partial result of every row and of every share of the
+ * prefix). */
 size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
                                        int64_t prefix_len);
 
 /* fa_decode_paged (without a window) for a batch whose sequences share a long prefix:
  * the first prefix_len / FA_BLOCK_SIZE entries of every row of page_table name the same
  * pages (a system prompt, the samples of one prompt), and the prefix is taken once for
- * all sequences.  Same result as fa_decode_paged.
+ * all sequences (unless it is so short or the batch so small that this takes longer).
+ * Same result as fa_decode_paged, up to rounding.
  *
  * In:  as fa_decode_paged; prefix_len >= 0, a multiple of FA_BLOCK_SIZE, at most
  *      pages_per_seq * FA_BLOCK_SIZE.  The shared entries are read from row 0 for the

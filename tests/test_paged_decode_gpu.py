@@ -260,6 +260,168 @@ def test_decode_shared_large_scores():
     assert_decode(got, decode_ref(q, k, v, table, lens, scale=1.0))
 
 
+# Prefixes that are taken once (the sizes above are taken page by page): one tile of rows,
+# pairs of tiles with a full and a partial second one and with a single one behind them,
+# odd numbers of pages, fewer columns than CTAs and more.
+ONCE = [
+    # batch, own lengths (cycled), prefix pages, q_len, Hq, Hkv, D, score
+    (49, (1, 130, 7), 17, 1, 8, 8, 128, None),
+    (40, (4, 300, 129), 79, 4, 8, 2, 64, "alibi"),
+    (70, (9, 128, 40, 5), 45, 4, 8, 2, 128, "softcap"),
+    (129, (2, 3, 200), 48, 2, 4, 1, 64, None),
+    (17, (60, 1), 385, 1, 16, 1, 128, "alibi"),
+    (2, (1, 2), 768, 1, 8, 8, 64, None),
+    (200, (1, 50), 4, 1, 8, 8, 64, "softcap"),
+    (4, (11000, 300, 7), 301, 4, 32, 8, 128, None),
+    (700, (1, 2, 140), 3, 1, 8, 8, 64, None),
+]
+
+
+def _once(own, B, pages):
+    return [PAGE * pages + own[i % len(own)] for i in range(B)]
+
+
+def _assert_taken_once(fa, q, k, prefix):
+    lib, B, Hkv = fa.library(), q.shape[0], k.shape[1]
+    assert lib.fa_decode_shared_workspace_size(B, q.shape[1], Hkv, q.shape[2], q.shape[3], prefix) > \
+        lib.fa_decode_paged_workspace_size(B, q.shape[1], Hkv, q.shape[2], q.shape[3])
+
+
+@pytest.mark.parametrize("case", ONCE, ids=lambda c: f"b{c[0]}-p{c[2]}-n{c[3]}-h{c[4]}-{c[5]}-d{c[6]}-{c[7]}")
+def test_decode_shared_prefix_taken_once(case):
+    fa = _fa()
+    B, own, pages, n, Hq, Hkv, D, kind = case
+    lens, prefix = _once(own, B, pages), PAGE * pages
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=B + D, prefix=prefix, filler=float("nan"))
+    _assert_taken_once(fa, q, k, prefix)
+    score = _score(kind, Hq)
+    args = [t.cuda() for t in (q, k, v, table, sl)]
+    tab = args[3].clone()
+    tab[1:, :pages] = 0  # the shared entries are those of row 0
+    got = fa.flex_decode_shared(*args[:3], tab, args[4], prefix, score_mod=_gpu(score))
+    assert_decode(got, decode_ref(q, k, v, table, lens, None, score))
+    for _ in range(10):
+        again = fa.flex_decode_shared(*args, prefix, score_mod=_gpu(score))
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
+
+
+def test_decode_shared_once_with_short_sequences():
+    """Sequences that end in the prefix (with pages of their own), reach only just past it,
+    or are empty, among those that share it."""
+    fa = _fa()
+    B, pages, n, Hq, Hkv, D = 200, 4, 3, 16, 8, 64
+    prefix = PAGE * pages
+    lens = [(700, 512, 100, 0, 514, 515, 2, 1000)[i % 8] for i in range(B)]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=3, prefix=prefix, filler=float("nan"))
+    _assert_taken_once(fa, q, k, prefix)
+    table[2, 0] = int(table[0, 4])
+    got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), prefix,
+                                score_mod=("softcap", 5.0))
+    assert_decode(got, decode_ref(q, k, v, table, lens, None, ("softcap", 5.0)))
+    none = torch.zeros_like(sl)
+    o, lse = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), none.cuda(), prefix)
+    assert not bool(o.any()) and bool(torch.isneginf(lse).all())
+    assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_shared_once_large_and_infinite_scores(D):
+    """Scores that grow along the prefix by many rescaling steps; then keys of the prefix
+    that are minus infinity for every row, and an infinite value."""
+    fa = _fa()
+    B, pages, Hq, Hkv = 60, 14, 8, 8
+    prefix = PAGE * pages
+    lens = _once((5, 140), B, pages)
+    q, k, v, table, sl = paged_case(lens, 1, Hq, Hkv, D, seed=15, prefix=prefix)
+    _assert_taken_once(fa, q, k, prefix)
+    q[:] = 1.0
+    g = torch.Generator().manual_seed(4)
+    for t in range(pages):
+        k[int(table[0, t])] = (0.25 * (t % 9) + 0.001 * torch.randn((Hkv, PAGE, D), generator=g)).to(torch.bfloat16)
+    k[int(table[0, 5]), :, 64:] = -3.0
+    got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), prefix, scale=1.0)
+    assert_decode(got, decode_ref(q, k, v, table, lens, scale=1.0))
+    k[int(table[0, 2]), :, :70] = float("-inf")
+    k[int(table[0, 0])] = float("-inf")
+    got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), prefix, scale=1.0)
+    ref = decode_ref(q, k, v, table, lens, scale=1.0)
+    ref = ref[0], ref[1], ref[2].nan_to_num(0.0), ref[3]
+    # the bound of a score's own error is infinite there; 2^-7 covers P's rounding and 2 e of
+    # the finite scores (|x| <= 2.1 D: e <= D 2^-23 2.1 D + 2^-16 < 2^-7.8)
+    v_size = v.abs().max().double()
+    assert bool(((got[0].cpu().double() - ref[0]).abs() <= (2 ** -8 + 2 * 2 ** -7.8 + 2 ** -8) * v_size).all())
+    v[int(table[0, 9]), 3, 17, 5] = float("inf")
+    got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), prefix)
+    assert bool(torch.isinf(got[0][:, 3, 0, 5]).all())
+    rest = torch.ones_like(got[0], dtype=torch.bool)
+    rest[:, 3, 0, 5] = False
+    assert bool(torch.isfinite(got[0][rest]).all())
+
+
+def test_decode_shared_once_views_and_reports():
+    """Token-major queries and outputs, a bad page in the prefix (clamped and reported),
+    and the next call on the same workspace clean."""
+    fa = _fa()
+    B, pages, n, Hq, Hkv, D = 52, 30, 2, 8, 4, 128
+    prefix = PAGE * pages
+    lens = _once((9, 1, 300), B, pages)
+    lens = [x + 1 for x in lens]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=5, prefix=prefix)
+    kp, vp, tab, ln = k.cuda(), v.cuda(), table.cuda(), sl.cuda()
+    qt = q.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    out = torch.full((B, n, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    size = fa.library().fa_decode_shared_workspace_size(B, Hq, Hkv, n, D, prefix)
+    ws = torch.zeros(int(size), dtype=torch.uint8, device="cuda")
+    bad = tab.clone()
+    bad[0, 3], bad[0, 11] = -4, k.shape[0] + 9
+    fa.flex_decode_shared(qt, kp, vp, bad, ln, prefix, out=out, ws=ws)
+    assert fa.device_status(ws=ws) == fa.FA_ERR_BAD_BLOCKMASK
+    got = fa.flex_decode_shared(qt, kp, vp, tab, ln, prefix, scale=0.05, out=out, ws=ws)
+    assert fa.device_status(ws=ws) == 0 and got[0] is out
+    assert_decode(got, decode_ref(q, k, v, table, lens, scale=0.05))
+    with pytest.raises(fa.FlexAttnError):
+        fa.flex_decode_shared(qt, kp, vp, tab, ln, prefix, ws=ws[:-16])
+
+
+def test_decode_shared_once_in_graphs_and_on_streams():
+    """Two captured calls replayed on two streams at once beside an eager one, their
+    lengths changed in place (and with them the kernel's split of the SMs)."""
+    fa = _fa()
+    cases = []
+    for B, pages, Hq, Hkv, D in ((49, 17, 8, 8, 64), (30, 55, 8, 4, 128)):
+        lens = _once((700, 3, 90), B, pages)
+        c = paged_case(lens, 1, Hq, Hkv, D, seed=B, prefix=PAGE * pages)
+        cases.append((c, [t.cuda() for t in c], PAGE * pages))
+    graphs, outs = [], []
+    for c, d, prefix in cases:
+        fa.flex_decode_shared(*d, prefix)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fa.flex_decode_shared(*d, prefix))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for step in range(3):
+        lens = []
+        for c, d, prefix in cases:
+            x = c[4].clone()
+            if step:
+                x[::step] = prefix + 1 + step  # most sequences' own parts shrink
+            d[4].copy_(x)
+            lens.append(x.tolist())
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            eager = fa.flex_decode_shared(*cases[0][1], cases[0][2], stream=streams[2])
+        torch.cuda.synchronize()
+        for (c, d, prefix), o, x in zip(cases, outs, lens):
+            assert_decode(o, decode_ref(*c[:4], x), f"step {step}")
+        assert_decode(eager, decode_ref(*cases[0][0][:4], lens[0]), f"eager, step {step}")
+
+
 # ------------------------------------------------------------------ streams, graphs, refusals
 
 def test_decode_calls_on_two_streams_at_once():
