@@ -25,7 +25,6 @@ import contextlib
 import ctypes
 import functools
 import os
-import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -142,18 +141,14 @@ def _load():
     return lib
 
 
-def _load_packed():
-    """The serving calls with plain pointer arguments, which take a descriptor packed into
-    bytes: a step's call is short enough on the GPU for the binding's time to count."""
-    lib = ctypes.CDLL(LIB_PATH)
-    for name in ("fa_rope_apply", "fa_paged_append", "fa_decode_paged", "fa_decode_shared"):
-        getattr(lib, name).argtypes = [ctypes.c_void_p if hasattr(t, "contents") else t
-                                       for t in getattr(_lib, name).argtypes]
-    return lib
-
-
 _lib = _load()
-_packed = _load_packed()
+if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+    raise ImportError("_binding.so is missing: build it with `python block_sparse_attention_48_b200/build.py`")
+from . import _binding  # noqa: E402  (the serving calls' binding; needs torch loaded)
+
+_binding.bind(*[ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
+                ("fa_rope_apply", "fa_paged_append", "fa_decode_paged", "fa_decode_shared",
+                 "fa_decode_paged_workspace_size", "fa_decode_shared_workspace_size", "fa_workspace_size")])
 
 
 def library() -> ctypes.CDLL:
@@ -513,70 +508,17 @@ def flex_attention_autograd(q, k, v, block_mask: BlockMask, score_mod=None, scal
 
 # ------------------------------------------------------------------ rotary positions, paged cache
 
-_pack_tensor = struct.Struct("P8q").pack  # TensorDesc and RopeDesc as bytes
-_pack_rope = struct.Struct("Piif4x").pack
-assert struct.calcsize("P8q") == ctypes.sizeof(TensorDesc) and struct.calcsize("Piif4x") == ctypes.sizeof(RopeDesc)
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
-
-
-def _placed(fn):
-    """Run fn on the device of its first argument and, when given, on `stream` (fn's own
-    tensors are then allocated for that stream)."""
+def _on_stream(fn):
+    """Adds stream= to fn: the CUDA stream to run on (its own tensors are allocated for it)."""
     @functools.wraps(fn)
-    def call(x, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
-        if not (isinstance(x, torch.Tensor) and x.is_cuda):
-            raise TypeError(f"{fn.__name__}: expected CUDA tensors")
-        if stream is None and x.get_device() == torch._C._cuda_getDevice():
-            return fn(x, *args, **kw)
+    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
         if stream is None:
-            with torch.cuda.device(x.device):
-                return fn(x, *args, **kw)
-        if stream.device != x.device:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
+            return fn(*args, **kw)
+        if args[0].device != stream.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {args[0].device}")
         with torch.cuda.stream(stream):
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
     return call
-
-
-def _readable(t: torch.Tensor) -> torch.Tensor:
-    """t itself, or a contiguous copy where its strides or alignment are not ones the
-    kernels read (16-byte vectors along D, no expanded dimension)."""
-    if t.dim() == 4:
-        s0, s1, s2, s3 = t.stride()
-        if (s3 != 1 or (s0 | s1 | s2) & 7 or t.data_ptr() & 15 or not (s0 and s1 and s2)) and t.numel() and \
-                (s3 != 1 or (s0 | s1 | s2) & 7 or t.data_ptr() & 15 or _expanded(t)):
-            return t.contiguous() if not t.is_contiguous() else t.clone()
-    return t
-
-
-def _desc(t: torch.Tensor, device: torch.device, what: str) -> bytes:
-    if t.dtype is not torch.bfloat16 or t.dim() != 4 or t.device != device:
-        raise TypeError(f"{what}: expected a 4-D bf16 tensor on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return _pack_tensor(t.data_ptr(), *t.shape, *t.stride())
-
-
-def _ints(t: torch.Tensor, shape: tuple, device: torch.device, what: str) -> int:
-    """Address of an int32 tensor of the given shape (None: any size), its last dimension contiguous."""
-    have = t.shape
-    if t.dtype is not torch.int32 or t.device != device or len(have) != len(shape) or have[0] != shape[0] or \
-            (shape[-1] is not None and have[-1] != shape[-1]) or (t.stride(-1) != 1 and have[-1] > 1):
-        raise TypeError(f"{what}: expected int32 {list(shape)} on {device} with a contiguous last dimension, "
-                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _rope_desc(inv_freq: torch.Tensor, interleaved: bool, amplitude: float, device: torch.device) -> bytes:
-    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device or \
-            (inv_freq.shape[0] > 1 and inv_freq.stride(0) != 1):
-        raise TypeError(f"inv_freq: expected a contiguous fp64 tensor [rotary_dim / 2] on {device}")
-    if not amplitude > 0:
-        raise ValueError("amplitude must be positive")
-    return _pack_rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude)
-
-
-_paged_workspaces = {}
-_STATUS_BYTES = int(_lib.fa_workspace_size())
-_ZEROED_BYTES = 1 << 14  # more than the status word and the counters
 
 
 def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
@@ -586,26 +528,17 @@ def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
     graph is captured each call gets a workspace of the graph's own instead (pass ws= to
     read the status of captured calls), of which every replay zeroes the status word and
     the counters behind it."""
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty((max(need, _ZEROED_BYTES),), dtype=torch.uint8, device=device)
-        ws[:_ZEROED_BYTES].zero_()
-        return ws
-    index = device.index if device.index is not None else torch.cuda.current_device()
-    kept = _paged_workspaces.setdefault((index, _raw_stream(index)), [])
-    if not kept or kept[-1].numel() < need:
-        ws = torch.zeros((max(need, 1 << 22),), dtype=torch.uint8, device=device)
-        if kept:
-            ws[:_STATUS_BYTES].copy_(kept[-1][:_STATUS_BYTES])
-        kept.append(ws)
-    return kept[-1]
+    return _binding.workspace(device.index if device.index is not None else torch.cuda.current_device(), need)
 
 
-def _given_workspace(ws: torch.Tensor, need: int, device: torch.device, what: str) -> torch.Tensor:
-    if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise TypeError(f"{what}: ws must be a contiguous uint8 tensor on {device}")
-    if ws.numel() < need:
-        raise FlexAttnError(FA_ERR_INVALID_ARG, f"{what}: workspace of {ws.numel()} bytes, {need} needed")
-    return ws
+def _score(score_mod) -> tuple:
+    """(kind, slopes, softcap) of a score_mod for _binding.decode."""
+    if score_mod is None:
+        return 0, None, 0.0
+    kind = score_mod[0]
+    if kind not in SCORE:
+        raise ValueError(f"unknown score_mod {kind!r}")
+    return SCORE[kind], score_mod[1] if kind == "alibi" else None, score_mod[1] if kind == "softcap" else 0.0
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[tuple] = None,
@@ -629,7 +562,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[t
     return inv_freq.to(device if device is not None else "cuda"), amplitude.value
 
 
-@_placed
+@_on_stream
 def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
                positions: Optional[torch.Tensor] = None, interleaved: bool = False, amplitude: float = 1.0,
                inverse: bool = False, offset: int = 0, out: Optional[tuple] = None):
@@ -639,25 +572,9 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tenso
     offset + s).  inverse=True turns the other way, which takes the gradients of the
     outputs to those of q and k.  out: (q_out, k_out), which may be (q, k).  stream=:
     the CUDA stream to run on."""
-    device = q.device
-    rope = _rope_desc(inv_freq, interleaved, amplitude, device)
-    q = _readable(q)
-    k = _readable(k) if k is not None else None
-    if out is None:
-        out = (torch.empty_like(q), torch.empty_like(k) if k is not None else None)
-    q_out, k_out = out
-    if (k is None) != (k_out is None):
-        raise ValueError("rope_apply: out holds an output for each of q and k")
-    qd, qo = _desc(q, device, "q"), _desc(q_out, device, "out[0]")
-    kd, ko = (_desc(k, device, "k"), _desc(k_out, device, "out[1]")) if k is not None else (None, None)
-    pos, pos_stride = None, 0
-    if positions is not None:
-        B, S = q.shape[0], q.shape[2]
-        pos = _ints(positions, (S,) if positions.dim() == 1 else (B, S), device, "positions")
-        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    _check(_packed.fa_rope_apply(qd, kd, rope, pos, pos_stride, offset, 1 if inverse else 0, qo, ko,
-                                 _raw_stream(device.index)), "fa_rope_apply")
-    return out
+    q_out, k_out = out if out is not None else (None, None)
+    r = _binding.rope_apply(q, k, inv_freq, positions, interleaved, amplitude, inverse, offset, q_out, k_out)
+    return r if r.__class__ is tuple else _check(r, "fa_rope_apply")
 
 
 class RopeFunction(torch.autograd.Function):
@@ -684,7 +601,7 @@ def rope_autograd(q, k, inv_freq, positions=None, interleaved: bool = False, amp
     return out if k is not None else (out, None)
 
 
-@_placed
+@_on_stream
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  page_table: torch.Tensor, cache_lens: torch.Tensor, new_lens: Optional[torch.Tensor] = None,
                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -697,57 +614,12 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     cache_lens / new_lens int32 [B] are not changed.  Returns q_out (None without q;
     rows past new_lens are left as they were, zero in a q_out made here).  Bad lengths
     and pages: device_status(ws)."""
-    device = k.device
-    k, v = _readable(k), _readable(v)
-    B = k.shape[0]
-    kd, vd = _desc(k, device, "k"), _desc(v, device, "v")
-    kp, vp = _desc(k_pages, device, "k_pages"), _desc(v_pages, device, "v_pages")
-    table = _ints(page_table, (B, None), device, "page_table")
-    have = _ints(cache_lens, (B,), device, "cache_lens")
-    fresh = _ints(new_lens, (B,), device, "new_lens") if new_lens is not None else None
-    rope = _rope_desc(inv_freq, interleaved, amplitude, device) if inv_freq is not None else None
-    qd = qo = None
-    if q is not None:
-        q = _readable(q)
-        if q_out is None:
-            q_out = torch.empty_like(q) if new_lens is None else torch.zeros_like(q)
-        qd, qo = _desc(q, device, "q"), _desc(q_out, device, "q_out")
-    elif q_out is not None:
-        raise ValueError("paged_append: q_out without q")
-    ws = paged_workspace(device) if ws is None else _given_workspace(ws, _STATUS_BYTES, device, "fa_paged_append")
-    _check(_packed.fa_paged_append(kd, vd, qd, rope, have, fresh, table, page_table.stride(0), page_table.shape[1], kp,
-                                   vp, qo, ws.data_ptr(), ws.numel(), _raw_stream(device.index)), "fa_paged_append")
-    return q_out
+    r = _binding.paged_append(k, v, k_pages, v_pages, page_table, cache_lens, new_lens, q, q_out, inv_freq, interleaved,
+                              amplitude, ws)
+    return _check(r, "fa_paged_append") if r.__class__ is int else r
 
 
-def _decode_pages(name, fn, need, q, k_pages, v_pages, page_table, seq_lens, extra, score_mod, scale, out, lse, ws):
-    device = q.device
-    q = _readable(q)
-    B, Hq, n, D = q.shape
-    if out is None:
-        out = q.new_empty((B, Hq, n, D))
-    if lse is None:
-        lse = q.new_empty((B, Hq, n), dtype=torch.float32)
-    elif lse.dtype != torch.float32 or lse.device != device or lse.shape != (B, Hq, n) or not lse.is_contiguous():
-        raise TypeError(f"lse: expected a contiguous fp32 tensor [B, Hq, q_len] on {device}")
-    qd, od = _desc(q, device, "q"), _desc(out, device, "out")
-    kp, vp = _desc(k_pages, device, "k_pages"), _desc(v_pages, device, "v_pages")
-    table = _ints(page_table, (B, None), device, "page_table")
-    lens = _ints(seq_lens, (B,), device, "seq_lens")
-    sm = None
-    if score_mod is not None:
-        sm, _ = score_mod_desc(score_mod)
-        if score_mod[0] == "alibi" and (score_mod[1].shape != (Hq,) or score_mod[1].device != device):
-            raise TypeError(f"ALiBi slopes: fp32 [Hq] on {device}")
-        sm = bytes(sm)
-    ws = paged_workspace(device, need) if ws is None else _given_workspace(ws, need, device, name)
-    _check(fn(qd, kp, vp, table, page_table.stride(0), page_table.shape[1], lens, extra, sm,
-              scale if scale is not None else 0.0, od, lse.data_ptr(), ws.data_ptr(), ws.numel(),
-              _raw_stream(device.index)), name)
-    return out, lse
-
-
-@_placed
+@_on_stream
 def flex_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                       seq_lens: torch.Tensor, window: Optional[int] = None, score_mod=None,
                       scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
@@ -760,12 +632,12 @@ def flex_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     score_mod: None, ("alibi", slopes) or ("softcap", cap).  Returns (out, lse)."""
     if window is not None and window < 0:
         raise ValueError("flex_decode_paged: window must not be negative")
-    need = int(_lib.fa_decode_paged_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3]))
-    return _decode_pages("fa_decode_paged", _packed.fa_decode_paged, need, q, k_pages, v_pages, page_table, seq_lens,
-                         -1 if window is None else window, score_mod, scale, out, lse, ws)
+    r = _binding.decode(False, q, k_pages, v_pages, page_table, seq_lens, -1 if window is None else window,
+                        *_score(score_mod), 0.0 if scale is None else scale, out, lse, ws)
+    return r if r.__class__ is tuple else _check(r, "fa_decode_paged")
 
 
-@_placed
+@_on_stream
 def flex_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                        seq_lens: torch.Tensor, prefix_len: int, score_mod=None, scale: Optional[float] = None,
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -773,10 +645,9 @@ def flex_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     """flex_decode_paged for sequences that share their first prefix_len keys (a multiple
     of 128: the first prefix_len / 128 entries of every row of page_table are the same
     pages), which are taken once for the whole batch (fa_decode_shared)."""
-    need = int(_lib.fa_decode_shared_workspace_size(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], q.shape[3],
-                                                    prefix_len))
-    return _decode_pages("fa_decode_shared", _packed.fa_decode_shared, need, q, k_pages, v_pages, page_table, seq_lens,
-                         prefix_len, score_mod, scale, out, lse, ws)
+    r = _binding.decode(True, q, k_pages, v_pages, page_table, seq_lens, prefix_len, *_score(score_mod),
+                        0.0 if scale is None else scale, out, lse, ws)
+    return r if r.__class__ is tuple else _check(r, "fa_decode_shared")
 
 
 def device_status(ws: Optional[torch.Tensor] = None, device=None, stream=None) -> int:

@@ -1,4 +1,5 @@
-"""Build the CUDA library (libflexattn.so) in-tree with nvcc for sm_100a.
+"""Build the CUDA library (libflexattn.so) in-tree with nvcc for sm_100a, and the Python
+binding of the serving calls (_binding.so) with g++ against torch's headers.
 
     python block_sparse_attention_48_b200/build.py [--force] [--verbose]
 
@@ -10,9 +11,11 @@ from __future__ import annotations
 import argparse
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libflexattn.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -39,14 +44,31 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so (no CUDA code; torch is found without importing it)."""
+    if not force and not _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return BINDING
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc,
+                           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+                           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+                           BINDING_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
