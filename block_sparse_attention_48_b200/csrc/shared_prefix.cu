@@ -539,8 +539,7 @@ shared_decode_kernel(const __grid_constant__ SpParams p, const __grid_constant__
 }
 
 // The join: a lane a row and a warp four columns of 32, so that the partial results are
-// read in whole lines.  First the maximum over a row's parts, then their weighted sums:
-// no load waits for another part's.  The prefix's pieces come in list order, then the
+// read in whole lines; no load waits for another part's.  The prefix's pieces come in list order, then the
 // row's own part, whatever finished first.  Sequences that take no part in the sharing
 // were written by the paged decode.
 constexpr int kJoinWarps = 8, kJoinCols = 4 * kJoinWarps;
@@ -576,20 +575,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     if (takes) {
         const float2 last = __ldcg(reinterpret_cast<const float2*>(p.own_ml) + own);
         const float4 x = __ldcg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
-        M = last.x;
-#pragma unroll 8
-        for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(ml + k * step * kSpRows).x);
-        const float Mu = M == -INFINITY ? 0.f : M;
         auto take = [&](float2 w, float4 y) {
-            const float f = ex2_approx(w.x - Mu);
-            v[0] = fmaf(y.x, f, v[0]);
-            v[1] = fmaf(y.y, f, v[1]);
-            v[2] = fmaf(y.z, f, v[2]);
-            v[3] = fmaf(y.w, f, v[3]);
-            L = fmaf(w.y, f, L);
+            const float m = fmaxf(M, w.x), Mu = m == -INFINITY ? 0.f : m;
+            const float f0 = ex2_approx(M - Mu), f = ex2_approx(w.x - Mu);
+            M = m;
+            L = fmaf(w.y, f, L * f0);
+            v[0] = fmaf(y.x, f, v[0] * f0);
+            v[1] = fmaf(y.y, f, v[1] * f0);
+            v[2] = fmaf(y.z, f, v[2] * f0);
+            v[3] = fmaf(y.w, f, v[3] * f0);
         };
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) take(__ldcg(ml + k * step * kSpRows), __ldcg(po + k * step * (D / 4) * kSpRows));
+        for (int k = 0; k < parts; ++k)
+            take(__ldcg(ml + k * step * kSpRows), __ldcg(po + k * step * (D / 4) * kSpRows));
         take(last, x);
     }
     const bool some = L > 0.f && M != -INFINITY;
