@@ -1,13 +1,16 @@
 // Launch of a kernel whose CTAs may start before the stream's previous kernel has ended
-// (programmatic dependent launch): the kernel itself waits where it has to.
+// (programmatic dependent launch).  The kernel itself waits for that end before it reads or
+// writes anything (wait_prerequisites, by every thread); what is gained is the launch's
+// latency, and the start of CTAs on SMs that the previous kernel has left.
 #pragma once
 
 #include <cuda_runtime.h>
 
 namespace fa {
 
-template <class P>
-inline cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, P p)
+template <class... P>
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                const P&... p)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -19,7 +22,7 @@ inline cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, size_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p...);
 }
 
 } // namespace fa

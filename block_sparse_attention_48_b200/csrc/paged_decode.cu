@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "context.cuh"
+#include "dependent_launch.cuh"
 #include "paged_decode_impl.cuh"
 
 namespace fa {
@@ -43,6 +44,8 @@ __global__ void __launch_bounds__(kPdThreads, 1) paged_decode_kernel(const __gri
     __shared__ long long scratch[kPdThreads / 32];
     static_assert(pd::Cfg<D>::SMEM + sizeof(sh) + sizeof(scratch) <= 227 * 1024, "shared memory beyond 227 KB per CTA");
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    wait_prerequisites();
+    launch_dependents();
     bool bad = false;
     const pd::Scan scan = pd::scan_lengths<kPdThreads>(p, scratch, bad);
     pd::decode_cta<D, SCORE, NR, kPdThreads>(p, sh, smem, blockIdx.x, gridDim.x, scan, bad);
@@ -67,8 +70,7 @@ cudaError_t launch_variant(const PdParams& p, cudaStream_t stream)
             if (current_ctx(&key)) done.push_back(key);
         }
     }
-    kern<<<(unsigned)p.grid, kPdThreads, pd::Cfg<D>::SMEM, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(kern, dim3((unsigned)p.grid), kPdThreads, pd::Cfg<D>::SMEM, stream, p);
 }
 
 } // namespace

@@ -13,6 +13,7 @@
 // nearest whole number: at p = 10^6 a 32-bit product would be off by 0.06 radians.
 #include <cuda_runtime.h>
 
+#include "dependent_launch.cuh"
 #include "flex_fwd.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -58,6 +59,8 @@ __device__ __forceinline__ void turn(double pos, double f, float amp, float sgn,
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
 {
+    wait_prerequisites();
+    launch_dependents();
     constexpr int U = D / 16;                    // units per head
     constexpr int TOK = kRopeThreads / U;        // tokens per CTA
     const int u = threadIdx.x % U;
@@ -195,14 +198,9 @@ cudaError_t launch_rope(RopeParams& p, int D, int sms, cudaStream_t stream)
     p.first_chunk[0] = 0;
     for (int i = 0; i < kRopeGroups; ++i) p.first_chunk[i + 1] = p.first_chunk[i] + (p.g[i].H + per - 1) / per;
     const dim3 grid((unsigned)tiles, (unsigned)p.first_chunk[kRopeGroups]);
-    if (D == 64) {
-        if (p.interleaved) rope_kernel<64, true><<<grid, kRopeThreads, 0, stream>>>(p);
-        else rope_kernel<64, false><<<grid, kRopeThreads, 0, stream>>>(p);
-    } else {
-        if (p.interleaved) rope_kernel<128, true><<<grid, kRopeThreads, 0, stream>>>(p);
-        else rope_kernel<128, false><<<grid, kRopeThreads, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    auto kern = D == 64 ? (p.interleaved ? rope_kernel<64, true> : rope_kernel<64, false>)
+                        : (p.interleaved ? rope_kernel<128, true> : rope_kernel<128, false>);
+    return launch_after(kern, grid, kRopeThreads, 0, stream, p);
 }
 
 } // namespace fa

@@ -524,6 +524,7 @@ shared_decode_kernel(const __grid_constant__ SpParams p, const __grid_constant__
     static_assert(SharedSmem<D>::BYTES + sizeof(state) + sizeof(scratch) <= 227 * 1024,
                   "shared memory beyond 227 KB per CTA");
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    wait_prerequisites();
     launch_dependents();
     bool bad = false;
     const pd::Scan scan = pd::scan_lengths<kSpThreads>(own, scratch, bad);
@@ -623,8 +624,7 @@ cudaError_t launch_variant(const SpParams& p, const PdParams& own, cudaStream_t 
             if (current_ctx(&key)) done.push_back(key);
         }
     }
-    kern<<<(unsigned)p.sms, kSpThreads, SharedSmem<D>::BYTES, stream>>>(p, own);
-    return cudaGetLastError();
+    return launch_after(kern, dim3((unsigned)p.sms), kSpThreads, SharedSmem<D>::BYTES, stream, p, own);
 }
 
 } // namespace
