@@ -63,6 +63,17 @@ fa::RopeGroup rope_group(const fa_tensor* x, const fa_tensor* y, bool rotate, bo
     return g;
 }
 
+// The status of a launch; nothing is thrown through the C ABI.
+template <class Launch>
+int launched(Launch launch)
+{
+    try {
+        return launch() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    } catch (...) {
+        return FA_ERR_CUDA;
+    }
+}
+
 // Pools [num_pages, Hkv, FA_BLOCK_SIZE, D] of the same shape.
 int check_pools(const fa_tensor* k, const fa_tensor* v)
 {
@@ -329,7 +340,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.status = reinterpret_cast<int*>(ws);
     P.watchdog_ns = fa::watchdog_ns();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (prefix_pages == 0) return fa::launch_paged_decode(P, (int)D, kind, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if (prefix_pages == 0) return launched([&] { return fa::launch_paged_decode(P, (int)D, kind, st); });
 
     if (lay.sms < 2) return FA_ERR_UNSUPPORTED;
     P.own_ml = reinterpret_cast<float*>(ws + lay.own_ml);
@@ -359,8 +370,8 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     S.pt_width = P.pt_width;
     S.status = P.status;
     S.watchdog_ns = P.watchdog_ns;
-    if (fa::launch_shared_decode(S, P, (int)D, kind, st) != cudaSuccess) return FA_ERR_CUDA;
-    return fa::launch_shared_join(S, (int)D, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if ((rc = launched([&] { return fa::launch_shared_decode(S, P, (int)D, kind, st); })) != FA_OK) return rc;
+    return launched([&] { return fa::launch_shared_join(S, (int)D, st); });
 }
 
 } // namespace

@@ -8,6 +8,18 @@
 
 namespace fa {
 
+// The stream's next kernel may start its CTAs once every CTA of this one has called this.
+__device__ __forceinline__ void launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The previous kernel has ended, and what it wrote can be read.
+__device__ __forceinline__ void wait_prerequisites()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <class... P>
 inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                 const P&... p)

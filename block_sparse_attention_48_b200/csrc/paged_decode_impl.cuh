@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include "dependent_launch.cuh"
 #include "flex_fwd.cuh"
 #include "flexattn.h"
 #include "paged_decode.cuh"

@@ -46,21 +46,6 @@ __device__ __forceinline__ bool elect_one_sync()
     return pred != 0;
 }
 
-// ------------------------------------------------------------------ dependent launches
-
-// Kernels launched one after another by launch_after: the next grid's CTAs may start
-// once every CTA of this one has called launch_dependents, and what this grid wrote may
-// be read after wait_prerequisites (which waits for the previous grid's end).
-__device__ __forceinline__ void launch_dependents()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void wait_prerequisites()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count)

@@ -441,10 +441,11 @@ size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_
  *      that of the positions.  scale as fa_forward.
  *      workspace: >= fa_decode_paged_workspace_size(...) bytes, 16-byte aligned, its
  *      first 16 KB zeroed once before its first use; every call leaves it ready for the
- *      next, of any shape.  Calls that overlap in time need distinct workspaces.
- * Out: o [B, Hq, q_len, D] bf16, lse fp32 [B, Hq, q_len] or NULL; a row that attends
- *      nothing (a sequence of length 0, or a query token before its first key) gets
- *      O = 0, LSE = -inf.  The same inputs give the same bits.
+ *      next, of any shape (after FA_ERR_TIMEOUT zero it again).  Calls that overlap in
+ *      time need distinct workspaces.
+ * Out: o [B, Hq, q_len, D] bf16 (not overlapping an input), lse fp32 [B, Hq, q_len] or
+ *      NULL; a row that attends nothing (a sequence of length 0, or a query token before
+ *      its first key) gets O = 0, LSE = -inf.  The same inputs give the same bits.
  * Errors: as fa_decode; FA_ERR_UNSUPPORTED for more than 16 rows per kv head, a bias
  * score_mod or D, or B * Hkv * pages_per_seq of 2^31 - 256 and more.  A length below zero
  * or beyond pages_per_seq pages and a page outside the pool are clamped (no read outside
