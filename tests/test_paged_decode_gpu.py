@@ -473,6 +473,75 @@ def test_decode_graphs_replayed_with_new_lengths():
         assert_decode(outs[1], decode_ref(*b[:4], lens_b))
 
 
+def test_decode_of_a_large_batch():
+    """More sequences than a CTA has threads, many of them empty, and a table far wider
+    than any sequence needs."""
+    fa = _fa()
+    lens = [(i * 7) % 260 if i % 3 else 0 for i in range(5000)]
+    q, k, v, table, sl = paged_case(lens, 1, 2, 1, 64, seed=6, width=200)
+    got = fa.flex_decode_paged(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda())
+    assert_decode(got, decode_ref(q, k, v, table, lens))
+    with pytest.raises(fa.FlexAttnError):  # a work list of 2^31 pages
+        wide = torch.zeros((1, 1), dtype=torch.int32, device="cuda").expand(1, 2 ** 24 - 2)
+        many = torch.zeros((1, 256, 1, 64), dtype=torch.bfloat16, device="cuda")
+        pool = torch.zeros((1, 256, PAGE, 64), dtype=torch.bfloat16, device="cuda")
+        fa.flex_decode_paged(many, pool, pool, wide.contiguous(), sl[:1].cuda())
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_append_and_decode_chained_over_streams(captured):
+    """Each step appends on one stream and decodes on another, ordered by events, the
+    lengths advanced on the device in between: kernels that start before the stream's
+    previous kernel has ended still see everything before them.  Eagerly, and as one
+    captured graph that is replayed."""
+    fa = _fa()
+    B, Hq, Hkv, D, steps = 3, 8, 2, 64, 4
+    g = torch.Generator().manual_seed(12)
+    table = torch.randperm(24, generator=g)[:B * 4].view(B, 4).to(torch.int32).contiguous()
+    new = [[torch.randn((B, h, 1, D), generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv)] for _ in range(steps)]
+    start = [126, 3, 250]
+    kp0, vp0 = [torch.randn((24, Hkv, PAGE, D), generator=g).to(torch.bfloat16) for _ in range(2)]
+    f = 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)
+    kp, vp, tab, fd = kp0.cuda(), vp0.cuda(), table.cuda(), f.cuda()
+    dev = [[t.cuda() for t in step] for step in new]
+    have = torch.tensor(start, dtype=torch.int32, device="cuda")
+    ws = [torch.zeros(1 << 23, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def run():
+        outs = []
+        for q, k, v in dev:
+            qr = fa.paged_append(k, v, kp, vp, tab, have, q=q, inv_freq=fd, ws=ws[0])
+            have.add_(1)
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                outs.append((qr, *fa.flex_decode_paged(qr, kp, vp, tab, have, ws=ws[1])))
+            main.wait_stream(side)
+        return outs
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        if captured:
+            run()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                outs = run()
+            kp.copy_(kp0)
+            vp.copy_(vp0)
+            have.copy_(torch.tensor(start, dtype=torch.int32))
+            graph.replay()
+        else:
+            outs = run()
+    torch.cuda.synchronize()
+    assert fa.device_status(ws=ws[0]) == 0 and fa.device_status(ws=ws[1]) == 0
+    assert have.tolist() == [x + steps for x in start]
+    kc, vc = kp.cpu(), vp.cpu()
+    for i, (qr, o, lse) in enumerate(outs):
+        # later steps' keys lie behind this step's lengths
+        want = decode_ref(qr.cpu(), kc, vc, table, [x + i + 1 for x in start])
+        assert_decode((o, lse), want, f"step {i}")
+
+
 def test_decode_paged_refusals():
     fa = _fa()
     q, k, v, table, sl = [t.cuda() for t in paged_case([300, 20], 1, 8, 2, 64, seed=1)]
