@@ -12,11 +12,12 @@
 // and serve all of them.  The angle is reduced in 64 bits, p * f / (2 pi) less its
 // nearest whole number: at p = 10^6 a 32-bit product would be off by 0.06 radians.
 //
-// Measured on a B200: Q and K of 16383 tokens, Hq 32 Hkv 8 D 128 half rotated, token-major,
-// 51.8 us = 6.5 TB/s; four prompts of up to 4000 tokens appended with their rotated queries
-// 30 us = 6.8 TB/s; Q and K of B4 H16 S2048 D64 interleaved 12.7 us a launch = 5.3 TB/s (a
-// short kernel: the first loads wait for the angles of its few heads).  Angles computed by
-// the CTA for all its heads in shared memory: 70 us on the first.
+// Measured on a B200, calls back to back on changing inputs: Q and K of 16383 tokens, Hq 32
+// Hkv 8 D 128 half rotated, token-major, 54.9 us = 6.1 TB/s; four prompts of up to 4000 tokens
+// appended with their rotated queries 34.2 us = 6.0 TB/s; Q and K of B4 H16 S2048 D64
+// interleaved 13.7 us = 4.9 TB/s (a short kernel: its start and end are a fifth of it).  The
+// first loads are under way while the angles are computed (55.9 and 35.3 us after them).
+// Angles computed once per CTA, in shared memory: 70 us on the first.
 #include <cuda_runtime.h>
 
 #include "dependent_launch.cuh"
@@ -63,7 +64,7 @@ __device__ __forceinline__ void turn(double pos, double f, float amp, float sgn,
 // Interleaved: vectors u and u + D / 16, each with its own four pairs (so that a
 // warp reads consecutive vectors), rotated when below rotary / 8.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p)
 {
     wait_prerequisites();
     launch_dependents();
@@ -118,6 +119,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         va = u < half ? u : 2 * u;
         vb = u < half ? u + half : 2 * u + 1;
     }
+    src += 8 * va;
+    dst += 8 * va;
+    const int64_t d_vb = 8 * (int64_t)(vb - va);
+    uint4 xa[kRopeBatch], xb[kRopeBatch];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k)
+            if (h + k < h1) {
+                const uint16_t* q = src + (int64_t)(h + k) * g.x_st1;
+                xa[k] = *reinterpret_cast<const uint4*>(q);
+                xb[k] = *reinterpret_cast<const uint4*>(q + d_vb);
+            }
+    };
+    load(h0);  // under way while the angles are computed
     float c[8], sn[8];
     {
         const double dp = (double)pos;
@@ -140,18 +155,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             for (int i = 0; i < 8; ++i) turn(dp, __ldg(p.inv_freq + 8 * u + i), p.amplitude, p.sin_sign, c[i], sn[i]);
         }
     }
-    src += 8 * va;
-    dst += 8 * va;
-    const int64_t d_vb = 8 * (int64_t)(vb - va);
     for (int h = h0; h < h1; h += kRopeBatch) {
-        uint4 xa[kRopeBatch], xb[kRopeBatch];
-#pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k)
-            if (h + k < h1) {
-                const uint16_t* q = src + (int64_t)(h + k) * g.x_st1;
-                xa[k] = *reinterpret_cast<const uint4*>(q);
-                xb[k] = *reinterpret_cast<const uint4*>(q + d_vb);
-            }
+        if (h > h0) load(h);
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k)
             if (h + k < h1) {
@@ -190,17 +195,18 @@ cudaError_t launch_rope(RopeParams& p, int D, int sms, cudaStream_t stream)
 {
     const int tok = kRopeThreads / (D / 16);
     const int64_t tiles = (p.tokens + tok - 1) / tok;
-    // Heads per thread: many share one computed angle, few spread a small call over
-    // the SMs.  At least four CTAs per SM: Q and K of B4 H16 S2048 D64 take 12.6 us a
-    // launch; with at least eight (two heads a thread instead of four) 14.8.  Four heads'
-    // loads at a time: with eight 34.8 instead of 30.7 for that case forward and inverse.
+    // Heads per thread: many share one computed angle, few spread a small call over the
+    // SMs.  At least three CTAs per SM, as many as fit one: Q and K of B4 H16 S2048 D64,
+    // forward and inverse, take 27.4 us; with at least four (four heads a thread instead of
+    // eight) 28.7.  In 64 registers four CTAs would fit: 16383 tokens then take 63.4 us
+    // instead of 54.9.  Four heads' loads at a time: with eight the first case took 13 % more.
     int per = 16;
     auto chunks = [&](int n) {
         int c = 0;
         for (int i = 0; i < kRopeGroups; ++i) c += (p.g[i].H + n - 1) / n;
         return c;
     };
-    while (per > 1 && tiles * chunks(per) < (int64_t)4 * sms) per /= 2;
+    while (per > 1 && tiles * chunks(per) < (int64_t)3 * sms) per /= 2;
     p.heads_per_thread = per;
     p.first_chunk[0] = 0;
     for (int i = 0; i < kRopeGroups; ++i) p.first_chunk[i + 1] = p.first_chunk[i] + (p.g[i].H + per - 1) / per;
