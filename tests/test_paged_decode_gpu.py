@@ -145,6 +145,32 @@ def test_decode_with_many_pages_a_cta(shape, shared):
     assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
 
 
+@pytest.mark.parametrize("shape", [(8, 8, 128, 1, None, None), (8, 8, 64, 2, None, "softcap"),
+                                   (32, 8, 128, 4, 30000, "alibi")])
+def test_decode_of_long_lists_on_streams(shape):
+    """A dozen pages and more a team: calls one after another, on one workspace and on two
+    streams at once, give the same bits."""
+    fa = _fa()
+    Hq, Hkv, D, n, window, kind = shape
+    lens = [47003, 2, 13000, 0, 130, 36000]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=78, filler=float("nan"))
+    score = _score(kind, Hq)
+    args = [t.cuda() for t in (q, k, v, table, sl)]
+    kw = dict(window=window, score_mod=_gpu(score))
+    got = fa.flex_decode_paged(*args, **kw)
+    assert_decode(got, decode_ref(q, k, v, table, lens, window, score))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(40):
+        outs.append(fa.flex_decode_paged(*args, **kw) if i % 4 == 0 else
+                    fa.flex_decode_paged(*args, stream=streams[i % 2], **kw))
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, got[0]) and torch.equal(lse, got[1])
+    assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
+
+
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length"])
 def test_decode_paged_reports_bad_tables_and_lengths(what, shared):
