@@ -397,7 +397,7 @@ int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tenso
 size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
                                        int64_t prefix_len)
 {
-    if (prefix_len < 0 || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
+    if (prefix_len < 0 || prefix_len > kMaxLen || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
     const int64_t pages = prefix_len / FA_BLOCK_SIZE;
     return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, pages) ? pages : 0).end;
