@@ -21,13 +21,14 @@
 // not depend on who comes last.
 //
 // Measured on a B200 (back to back, inputs not in L2): 8 sequences of 24k to 32k keys, Hkv 8
-// D 128, 139 us = 6.5 TB/s; 16 ragged ones up to 8191 keys 47 us; 24 with four drafted
-// tokens, a window of 4096 and capped scores, Hkv 8 D 64, 42 us; one of 700 keys 8.3 us.
+// D 128, 137 us = 6.6 TB/s; 16 ragged ones up to 8191 keys 45 us; 24 with four drafted
+// tokens, a window of 4096 and capped scores, Hkv 8 D 64, 40 us; one of 700 keys 8.3 us.
 // What the short ones are over their bytes is the start (the lengths, the table and the
 // first pages one after the other, 4 us), unequal shares of the memory's bandwidth (the
 // last SM ends 5 us after the first) and the join of split segments (4 us).  Tried and
 // slower: eight warps of 16 keys on every page (0.85 us a page, more than the 32 KB of one
-// at D = 64 need); two groups of warps on alternate pages of one share (they wait for one
+// at D = 64 need); an eighth of the list left open and taken by teams as they get done; two
+// groups of warps on alternate pages of one share (they wait for one
 // another at every segment's end); more than 192 KB in flight per SM.
 //
 // Places outside a row's keys may hold anything (a page's slots behind the last key
