@@ -266,6 +266,20 @@ bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t prefix_pages)
     return (B - 1) * Hkv * prefix_pages >= 6144;
 }
 
+// Teams for at most T pages in `segments` segments: all `most` of them, unless few segments
+// would be cut into more pieces than pay.  With n teams a team takes about T / n us, and a
+// segment's last team 60 ns for each of its n / segments pieces and 512 of a piece's floats:
+// the sum is least at n^2 = 1000 T segments / that cost and flat around it, so n^2 up to
+// twice that stays.  All / the fewer teams, us on a B200: 60.2 / 25.1 for one segment of 30000
+// keys (8 rows, D 128), 40.5 / 34.2 for 6 of 3003 to 12940 (16 rows, D 128), and 14.2 / 14.4
+// for 9 of 4400 (D 64), which keep theirs.  (T is the page table's, not the lengths': counted
+// on the device the rule cost every call 0.3 us.)
+int32_t teams_that_pay(int64_t T, int64_t segments, int64_t floats, int64_t most)
+{
+    const double n = std::sqrt(2000.0 * (double)T * (double)segments / (60.0 * (double)((floats + 511) / 512)));
+    return n < (double)most ? n < 1.0 ? 1 : (int32_t)n : (int32_t)most;
+}
+
 // fa_decode_paged and fa_decode_shared (prefix_len > 0).
 int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
                  int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
@@ -333,6 +347,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.slopes = kind == FA_SCORE_ALIBI ? sm->alibi_slopes : nullptr;
     const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more than pages in all
     P.grid = (int32_t)(most < 1 ? 1 : most < lay.sms ? most : lay.sms);
+    P.teams = teams_that_pay(most, B * Hkv, (int64_t)P.rows * D, lay.sms * fa::kPdTeams);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     P.part_ml = reinterpret_cast<float*>(ws + lay.ml);

@@ -24,6 +24,7 @@ struct PdParams {
     float* lse;         // [B, Hq, q_len] or null
 
     int32_t B, Hq, Hkv, G, q_len, rows;
+    int32_t teams;              // at most so many have work
     const int32_t* seq_lens;    // [B]
     const int32_t* page_table;  // row b at b * pt_stride, pt_width entries
     int64_t pt_stride;

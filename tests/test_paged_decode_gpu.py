@@ -244,6 +244,31 @@ def test_decode_shared_matches_the_formula(case):
     assert torch.equal(bits[0], got[0]) and torch.equal(bits[1], got[1])
 
 
+@pytest.mark.parametrize("case", [
+    # lens, q_len, Hq, Hkv, D, score: few segments of many pages, whose pieces one team joins
+    ([21000], 1, 1, 1, 64, None),
+    ([30011], 1, 16, 1, 128, "softcap"),
+    ([12345, 9000], 2, 8, 1, 128, None),
+    ([25000, 1, 0, 3100], 5, 6, 2, 64, "alibi"),
+    ([16500, 12], 3, 5, 1, 128, None),
+], ids=lambda c: "-".join(str(x) for x in c)[:60])
+def test_decode_of_few_long_sequences(case):
+    """Every row's pieces of a long sequence, joined by one team, with a table of just the
+    pages and one that is much wider; the same bits every time."""
+    fa = _fa()
+    lens, n, Hq, Hkv, D, kind = case
+    score, pages = _score(kind, Hq), (max(lens) + PAGE - 1) // PAGE
+    for width in (None, 4 * pages):
+        q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=len(lens) + D, width=width, filler=float("nan"))
+        args = [t.cuda() for t in (q, k, v, table, sl)]
+        got = fa.flex_decode_paged(*args, score_mod=_gpu(score))
+        assert_decode(got, decode_ref(q, k, v, table, lens, None, score))
+        for _ in range(5):
+            again = fa.flex_decode_paged(*args, score_mod=_gpu(score))
+            assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert fa.device_status(ws=fa.paged_workspace(DEV)) == 0
+
+
 def test_decode_shared_with_short_sequences():
     """Sequences that end inside the prefix, or whose first query tokens lie in it, are
     taken from their own rows (which may name other pages); empty ones give zeros."""
