@@ -535,8 +535,12 @@ shared_decode_kernel(const __grid_constant__ SpParams p, const __grid_constant__
     launch_dependents();
     bool bad = false;
     const pd::Scan scan = pd::scan_lengths<kSpThreads>(own, scratch, bad);
+    // An entry's softmax takes twice as long with the soft cap's tanh.  Entries at 16 / at 32
+    // with it, us on a B200 with cold caches: 53.4 / 40.0 (B64 Hkv8 G4 D128, 4096 shared keys),
+    // 77.5 / 53.4 (B64 Hkv16, 6 rows, D64, 4608), 40.7 / 43.9 (B40 Hkv4, 16 rows, D64, 8192).
+    constexpr int kEntryCost = SCORE == FA_SCORE_SOFTCAP ? 32 : 16;
     const int ctas = sp_split(p.Hkv * p.geom.per_head, p.Hkv * sp_cols(p.geom), pd::Scan::pages(scan.total) * p.Hkv,
-                              pd::Scan::sequences(scan.total) * p.Hkv, gridDim.x);
+                              pd::Scan::sequences(scan.total) * p.Hkv, gridDim.x, kEntryCost);
     if ((int)blockIdx.x < ctas) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.split = ctas;
         prefix_cta<D, SCORE>(p, reinterpret_cast<State*>(state)->sp, smem, blockIdx.x, ctas);

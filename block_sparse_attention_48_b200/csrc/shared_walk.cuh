@@ -81,11 +81,11 @@ FA_SP_FN int sp_start(const SpGeom& g, int hk, int col) { return hk * g.per_head
 // proportion to the two lists' costs, so that both end together, and if that is near a
 // multiple of the columns, that multiple: no share then runs over two columns, whose end
 // and start cost a CTA as much as four entries.  The same on every CTA of both kernels.
-// In tenths of a microsecond of an SM: an entry 16, a page 5, and 10 for a segment's start
-// and end.
-FA_SP_FN int sp_split(int entries, int columns, int own_pages, int own_segments, int sms)
+// In tenths of a microsecond of an SM: an entry `entry_cost`, a page 5, and 10 for a
+// segment's start and end.
+FA_SP_FN int sp_split(int entries, int columns, int own_pages, int own_segments, int sms, int entry_cost)
 {
-    const float a = 16.f * entries, b = 5.f * own_pages + 10.f * own_segments;
+    const float a = (float)entry_cost * entries, b = 5.f * own_pages + 10.f * own_segments;
     const int most = entries < sms - 1 ? entries : sms - 1;
     int n = a > 0.f ? (int)(sms * (a / (a + b)) + 0.5f) : 1;
     n = n < most ? n : most;

@@ -74,6 +74,11 @@ extern "C" long long fa_host_pd_walk(int32_t B, int32_t Hkv, int32_t q_len, int3
 
 extern "C" int fa_host_pd_holder(long long T, long long x, int used) { return fa::pd_holder(T, x, used); }
 
+extern "C" int fa_host_sp_split(int entries, int columns, int own_pages, int own_segments, int sms, int entry_cost)
+{
+    return fa::sp_split(entries, columns, own_pages, own_segments, sms, entry_cost);
+}
+
 extern "C" int fa_host_pd_page(int page, int num_pages, int32_t* bad)
 {
     bool b = false;

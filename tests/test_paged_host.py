@@ -334,6 +334,17 @@ def test_shared_prefix_work_list(lib, R, pages, Hkv):
                 assert holders[(hk, col)] == list(range(c0, c1 + 1))
 
 
+@pytest.mark.parametrize("cost", [16, 32])
+def test_split_of_the_sms(lib, cost):
+    """Both lists get an SM whatever their sizes; whatever an entry costs."""
+    for entries in (1, 5, 576, 10 ** 6):
+        for columns in (1, 4, 48, 300):
+            for pages, segments in ((0, 0), (1, 1), (1024, 1024), (10 ** 6, 10)):
+                for sms in (2, 7, 148):
+                    n = lib.fa_host_sp_split(entries, columns, pages, segments, sms, cost)
+                    assert 1 <= n <= sms - 1 and n <= max(entries, 1)
+
+
 def test_workspace_sizes():
     lib = fa.library()
     assert lib.fa_decode_paged_workspace_size(0, 8, 2, 1, 64) == 256
