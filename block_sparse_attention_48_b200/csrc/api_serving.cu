@@ -258,12 +258,15 @@ PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t pref
 
 // Whether a shared prefix is taken once, by the kernel made for it, or page by page for
 // every sequence.  The first costs some 15 us more before it reads anything; the second
-// reads (B - 1) Hkv prefix_pages pages again, most of them from L2.  Once / page by page, us
-// on a B200 with cold caches: 33.9 / 25.8 at 2816 such pages (B12 Hkv8 G4 D128, 4096 keys),
-// 34.2 / 38.6 at 5888 (B24), 30.1 / 30.5 at 6016 (B48 Hkv4 G4 D64), 37.6 / 63.3 at 12032 (B48).
-bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t prefix_pages)
+// reads (B - 1) Hkv prefix_pages pages again, most of them from L2, and is slower the more a
+// page costs it.  Page by page / once, us on a B200: to 8 rows, D 128, 21.3 / 24.3 at 1976
+// such pages, 30.3 / 30.4 at 3952, 33.8 / 31.0 at 4096; D 64, 24.8 / 28.6 at 3952, 30.5 / 30.1
+// at 6016; to 16 rows, D 128, 33.0 / 25.7 at 896, 41.1 / 34.8 at 1976; D 64, 26.2 / 28.1 at
+// 1976, 36.1 / 29.8 at 3952.
+bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
 {
-    return (B - 1) * Hkv * prefix_pages >= 6144;
+    const int64_t least = D == 128 ? (rows > 8 ? 1024 : 4096) : rows > 8 ? 2048 : 6144;
+    return (B - 1) * Hkv * prefix_pages >= least;
 }
 
 // Teams for at most T pages in `segments` segments: all `most` of them, unless few segments
@@ -309,7 +312,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;
     if (prefix_pages > 0 && Hkv * (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
         return FA_ERR_UNSUPPORTED;
-    const int64_t row0_pages = takes_prefix_once(B, Hkv, prefix_pages) ? 0 : prefix_pages;
+    const int64_t row0_pages = takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages) ? 0 : prefix_pages;
     if (row0_pages) prefix_pages = 0;
     const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
     if (lay.sms <= 0) return FA_ERR_CUDA;
@@ -415,7 +418,7 @@ size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64
     if (prefix_len < 0 || prefix_len > kMaxLen || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
     const int64_t pages = prefix_len / FA_BLOCK_SIZE;
-    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, pages) ? pages : 0).end;
+    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, pages) ? pages : 0).end;
 }
 
 int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,
