@@ -370,9 +370,11 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
     // of one) can be split; both arrive at the share's end, where the fence's and the
     // counters' latency holds up nothing.
     auto join_parts = [&](const PdWalk& at, int c0, int c1) {
-        // Items under way together: two where there are more than the team's threads (16 rows,
-        // 12 segments of 12000 keys: 53.3 us one by one, 41.7 so).
-        constexpr int TH = 32 * kPdWarps, I = NR, U = NR == 1 ? 4 : 8;
+        // Items under way together: all of up to 16 rows, and 16 loads of a thread (12 segments
+        // of 12000 keys, 16 rows, D 128: 53.3 us one by one, 41.7 two by two, 40.6 so; 24 and
+        // 32 loads: 41.8 and 42.9).  Up to 8 rows are mostly one item; two by two, their code
+        // cost every call 0.7 us and more.
+        constexpr int TH = 32 * kPdWarps, I = NR == 1 ? 1 : D / 32, U = NR == 1 ? 4 : 16 / I;
         const int items = p.rows * (D / 4);  // four columns of a row
         for (int it0 = tid; it0 < items; it0 += I * TH) {
             float M[I], L[I], v[I][4];
@@ -404,7 +406,7 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
             }
 #pragma unroll
             for (int i = 0; i < I; ++i)
-                if (i == 0 || it0 + TH < items) write_out(at.b, at.hk, r[i], d[i], at.r.shared, M[i], L[i], v[i]);
+                if (it0 + i * TH < items) write_out(at.b, at.hk, r[i], d[i], at.r.shared, M[i], L[i], v[i]);
         }
     };
 
