@@ -269,18 +269,22 @@ bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t 
     return (B - 1) * Hkv * prefix_pages >= least;
 }
 
-// Teams for at most T pages in `segments` segments: all `most` of them, unless few segments
-// would be cut into more pieces than pay.  With n teams a team takes about T / n us, and a
-// segment's last team 60 ns for each of its n / segments pieces and 512 of a piece's floats:
-// the sum is least at n^2 = 1000 T segments / that cost and flat around it, so n^2 up to
-// twice that stays.  All / the fewer teams, us on a B200: 60.2 / 25.1 for one segment of 30000
-// keys (8 rows, D 128), 40.5 / 34.2 for 6 of 3003 to 12940 (16 rows, D 128), and 14.2 / 14.4
-// for 9 of 4400 (D 64), which keep theirs.  (T is the page table's, not the lengths': counted
-// on the device the rule cost every call 0.3 us.)
-int32_t teams_that_pay(int64_t T, int64_t segments, int64_t floats, int64_t most)
+// Teams for `segments` segments of at most `pages` pages: all `most` of them, unless few
+// segments would be cut into more pieces than pay.  With n teams a team takes about T / n us
+// for T pages, and a segment's last team `cost` ns for each of its n / segments pieces: the
+// sum is least at n^2 = 1000 T segments / cost.  The pieces are then of whole pages and as
+// many for every segment, so that no share runs over two segments of equal length.  All / the
+// fewer teams, us on a B200: one segment of 30000 keys (8 rows, D 128) 60.1 / 22.3; 2 of 8000 (4
+// rows, D 64) 14.8 / 11.2; 2 of 60000 (16 rows, D 128) 52.0 / 34.8; 8 of 8000 (16 rows, D 128)
+// 26.7 / 22.0; 9 of 3746 to 4998 (4 rows, D 64) 14.2 / 15.3.  (By the page table's width: a
+// rule on the lengths themselves, on the device, cost every call 0.3 us.)
+int32_t teams_that_pay(int64_t segments, int64_t pages, int64_t rows, int64_t D, int64_t most)
 {
-    const double n = std::sqrt(2000.0 * (double)T * (double)segments / (60.0 * (double)((floats + 511) / 512)));
-    return n < (double)most ? n < 1.0 ? 1 : (int32_t)n : (int32_t)most;
+    const double cost = rows > 8 ? 50.0 * (double)D / 64 : 45.0 * (double)((rows * D + 511) / 512);
+    const double pieces = std::sqrt(1000.0 * (double)pages / cost);  // of a segment
+    if (!(pieces * (double)segments < (double)most) || pieces >= (double)pages) return (int32_t)most;
+    const int64_t m = pieces < 1.0 ? 1 : (int64_t)pieces, share = (pages + m - 1) / m;
+    return (int32_t)(segments * ((pages + share - 1) / share));
 }
 
 // fa_decode_paged and fa_decode_shared (prefix_len > 0).
@@ -350,7 +354,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.slopes = kind == FA_SCORE_ALIBI ? sm->alibi_slopes : nullptr;
     const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more than pages in all
     P.grid = (int32_t)(most < 1 ? 1 : most < lay.sms ? most : lay.sms);
-    P.teams = teams_that_pay(most, B * Hkv, (int64_t)P.rows * D, lay.sms * fa::kPdTeams);
+    P.teams = teams_that_pay(B * Hkv, pages_per_seq, P.rows, D, lay.sms * fa::kPdTeams);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     P.part_ml = reinterpret_cast<float*>(ws + lay.ml);
