@@ -13,15 +13,22 @@ struct PdRange {
     int32_t shared;  // the pages before lo are the shared prefix, taken elsewhere
 };
 
-// A length below zero or beyond the table's pages is clamped and sets `bad`.
+// A sequence's length: one below zero or beyond the table's pages (whose keys are fewer than
+// 2^31) is clamped.  The same in every kernel that reads it.
+template <class P>
+__device__ __forceinline__ int32_t pd_length(const P& p, int32_t raw_len)
+{
+    const int32_t most = p.pt_width * 128;
+    return raw_len < 0 ? 0 : raw_len > most ? most : raw_len;
+}
+
+// A clamped length sets `bad`.
 template <class P>
 __device__ __forceinline__ PdRange pd_range(const P& p, int32_t raw_len, bool& bad)
 {
     PdRange r;
-    int64_t len = raw_len;
-    if (len < 0) { bad = true; len = 0; }
-    if (len > (int64_t)p.pt_width * 128) { bad = true; len = (int64_t)p.pt_width * 128; }
-    r.len = (int32_t)len;
+    const int64_t len = r.len = pd_length(p, raw_len);
+    bad |= r.len != raw_len;
     const int64_t pos = len - p.q_len;  // of the first query token
     // a prefix that every query token attends whole is left out; n > 0 all the same,
     // since pos >= 128 prefix_pages and q_len > 0

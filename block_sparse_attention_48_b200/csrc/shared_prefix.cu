@@ -349,7 +349,7 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
         int pos = 0;
         if (SCORE == FA_SCORE_ALIBI && valid) {
             slope2 = __ldg(p.slopes + pc.hk * p.G + g) * kLog2e;
-            pos = __ldg(p.seq_lens + b) - p.q_len + qi;
+            pos = pd_length(p, __ldg(p.seq_lens + b)) - p.q_len + qi;
         }
         float m_run = -INFINITY, l_run = 0.f;
         // a warp without rows only passes the barriers on (its rows of P and O are nobody's)
@@ -567,8 +567,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const bool in = R < p.geom.rows;
     const int b = in ? R / p.rows : 0, j = in ? R - b * p.rows : 0;
     const int hq = hk * p.G + j / p.q_len, i = j % p.q_len;
-    const int64_t most = (int64_t)p.pt_width * 128, raw = __ldg(p.seq_lens + b), len = raw < most ? raw : most;
-    const bool takes = in && len - p.q_len >= (int64_t)p.geom.pages * 128;
+    const bool takes = in && (int64_t)pd_length(p, __ldg(p.seq_lens + b)) - p.q_len >= (int64_t)p.geom.pages * 128;
     const int col = R / (2 * kSpRows), r = R % kSpRows;  // the same column and tile in all lanes
     const bool one = col >= p.geom.pairs;
     const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows;
