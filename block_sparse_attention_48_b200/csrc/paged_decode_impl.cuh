@@ -115,7 +115,7 @@ __device__ __forceinline__ Scan scan_lengths(const P& p, long long* scratch, boo
     s.lo = min(p.B, tid * per);
     s.hi = min(p.B, s.lo + per);
     s.mine = 0;
-    for (int b = s.lo; b < s.hi; ++b) s.mine += pd_weight(pd_range(p, __ldg(p.seq_lens + b), bad));
+    for (int b = s.lo; b < s.hi; ++b) s.mine += pd_weight(pd_range(p, p.seq_lens[b], bad));
     long long inc = s.mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -203,7 +203,7 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
                 chunk = w.t & ~31;
                 const int tt = chunk + lane;
                 const int row = w.r.lo + tt < p.row0_pages && w.r.len - p.q_len >= 128 * p.row0_pages ? 0 : w.b;
-                page_lane = tt < w.r.n ? __ldg(p.page_table + row * p.pt_stride + w.r.lo + tt) : 0;
+                page_lane = tt < w.r.n ? p.page_table[row * p.pt_stride + w.r.lo + tt] : 0;
             }
             const int page = pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, w.t & 31), p.num_pages, bad);
             load(&p.tm_k, w.hk, page);
@@ -260,12 +260,12 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
         for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                slope[nt][j] = SCORE == FA_SCORE_ALIBI ? __ldg(p.slopes + hk * p.G + hq_g[nt][j]) * kLog2e : 0.f;
+                slope[nt][j] = SCORE == FA_SCORE_ALIBI ? p.slopes[hk * p.G + hq_g[nt][j]] * kLog2e : 0.f;
 #pragma unroll
             for (int kk = 0; kk < KD; ++kk) {
                 const uint16_t* src = seg + q_off[nt] + 16 * kk;
-                qb[nt][kk][0] = q_in[nt] ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
-                qb[nt][kk][1] = q_in[nt] ? __ldg(reinterpret_cast<const uint32_t*>(src + 8)) : 0u;
+                qb[nt][kk][0] = q_in[nt] ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+                qb[nt][kk][1] = q_in[nt] ? *reinterpret_cast<const uint32_t*>(src + 8) : 0u;
             }
         }
     };
@@ -392,8 +392,8 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
                 const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows;
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    const float2 w = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part + r[i]);
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + (part + r[i]) * D + d[i]));
+                    const float2 w = ld_cg(reinterpret_cast<const float2*>(p.part_ml) + part + r[i]);
+                    const float4 x = ld_cg(reinterpret_cast<const float4*>(p.part_o + (part + r[i]) * D + d[i]));
                     const float m = fmaxf(M[i], w.x), Mu = m == -INFINITY ? 0.f : m;
                     const float f0 = ex2_approx(M[i] - Mu), f = ex2_approx(w.x - Mu);
                     M[i] = m;
@@ -708,7 +708,7 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
     }
     // sequences without a key: O = 0, LSE = -inf
     for (int b = block; b < p.B; b += ctas) {
-        if (pd_range(p, __ldg(p.seq_lens + b), bad).n > 0) continue;
+        if (pd_range(p, p.seq_lens[b], bad).n > 0) continue;
         const int per_head = p.q_len * (D / 8);
         for (int it = threadIdx.x; it < p.Hq * per_head; it += 32 * kPdWarps * kPdTeams) {
             const int h = it / per_head, i = it % per_head / (D / 8), u = it % (D / 8);

@@ -80,7 +80,7 @@ template <class P>
 __device__ __forceinline__ bool pd_find(const P& p, int x0, int lo, int hi, int before, PdWalk& w, bool& bad)
 {
     for (int b = lo; b < hi; ++b) {
-        const PdRange r = pd_range(p, __ldg(p.seq_lens + b), bad);
+        const PdRange r = pd_range(p, p.seq_lens[b], bad);
         if (x0 < p.Hkv * (before + r.n)) {
             const int off = x0 - p.Hkv * before;
             w = PdWalk{b, off / r.n, off % r.n, r};
@@ -102,7 +102,7 @@ __device__ __forceinline__ void pd_advance(const P& p, PdWalk& w, bool& bad)
     do {
         if (w.b + 1 >= p.B) { w.r.n = 0; return; }
         ++w.b;
-        w.r = pd_range(p, __ldg(p.seq_lens + w.b), bad);
+        w.r = pd_range(p, p.seq_lens[w.b], bad);
     } while (w.r.n == 0);
 }
 

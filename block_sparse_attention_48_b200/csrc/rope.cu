@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
     uint16_t* dst = g.y;
     int64_t pos;
     if (p.cache_lens) {
-        const int32_t have = __ldg(p.cache_lens + b);
-        int32_t fresh = p.new_lens ? __ldg(p.new_lens + b) : (int32_t)p.S;
+        const int32_t have = p.cache_lens[b];
+        int32_t fresh = p.new_lens ? p.new_lens[b] : (int32_t)p.S;
         // a bad length or page is reported and its tokens are left out: no write
         // outside the pools
         bool bad = have < 0 || fresh < 0 || fresh > p.S;
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
         pos = (int64_t)have + s;
         const int64_t slot_page = pos / 128;
         int32_t page = -1;
-        if (slot_page < p.pt_width) page = __ldg(p.page_table + b * p.pt_stride + slot_page);
+        if (slot_page < p.pt_width) page = p.page_table[b * p.pt_stride + slot_page];
         const bool lost = page < 0 || page >= p.num_pages;
         if ((bad || lost) && u == 0) atomicOr(p.status, STATUS_BAD_BLOCKMASK);
         if (lost) return;
         dst += g.paged ? (int64_t)page * g.y_st0 + (pos % 128) * g.y_st2 : b * g.y_st0 + s * g.y_st2;
     } else {
-        pos = p.positions ? (int64_t)__ldg(p.positions + b * p.pos_stride + s) : p.pos_offset + s;
+        pos = p.positions ? (int64_t)p.positions[b * p.pos_stride + s] : p.pos_offset + s;
         dst += b * g.y_st0 + s * g.y_st2;
     }
 
@@ -145,14 +145,14 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
             if (ra)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    turn(dp, __ldg(p.inv_freq + 4 * va + i), p.amplitude, p.sin_sign, c[i], sn[i]);
+                    turn(dp, p.inv_freq[4 * va + i], p.amplitude, p.sin_sign, c[i], sn[i]);
             if (rb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    turn(dp, __ldg(p.inv_freq + 4 * vb + i), p.amplitude, p.sin_sign, c[4 + i], sn[4 + i]);
+                    turn(dp, p.inv_freq[4 * vb + i], p.amplitude, p.sin_sign, c[4 + i], sn[4 + i]);
         } else if (ra) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) turn(dp, __ldg(p.inv_freq + 8 * u + i), p.amplitude, p.sin_sign, c[i], sn[i]);
+            for (int i = 0; i < 8; ++i) turn(dp, p.inv_freq[8 * u + i], p.amplitude, p.sin_sign, c[i], sn[i]);
         }
     }
     for (int h = h0; h < h1; h += kRopeBatch) {

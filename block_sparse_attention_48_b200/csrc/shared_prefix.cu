@@ -117,7 +117,7 @@ __device__ __forceinline__ void load_role(const SpParams& p, SpShared& sh, uint8
     auto page_at = [&](int t) {
         if (chunk != (t & ~31)) {
             chunk = t & ~31;
-            page_lane = chunk + lane < p.geom.pages ? __ldg(p.prefix_row + chunk + lane) : 0;
+            page_lane = chunk + lane < p.geom.pages ? p.prefix_row[chunk + lane] : 0;
         }
         return pd_page(__shfl_sync(0xFFFFFFFFu, page_lane, t & 31), p.num_pages, bad);
     };
@@ -334,7 +334,7 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
         for (int k = 0; k < U; ++k) {
             const int idx = k * 32 + lane;
             const unsigned long long src = __shfl_sync(0xFFFFFFFFu, mine, idx / U);
-            v[k] = src ? __ldg(reinterpret_cast<const uint4*>(src) + idx % U) : make_uint4(0, 0, 0, 0);
+            v[k] = src ? reinterpret_cast<const uint4*>(src)[idx % U] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -348,8 +348,8 @@ __device__ __forceinline__ void softmax_role(const SpParams& p, SpShared& sh, ui
         float slope2 = 0.f;
         int pos = 0;
         if (SCORE == FA_SCORE_ALIBI && valid) {
-            slope2 = __ldg(p.slopes + pc.hk * p.G + g) * kLog2e;
-            pos = pd_length(p, __ldg(p.seq_lens + b)) - p.q_len + qi;
+            slope2 = p.slopes[pc.hk * p.G + g] * kLog2e;
+            pos = pd_length(p, p.seq_lens[b]) - p.q_len + qi;
         }
         float m_run = -INFINITY, l_run = 0.f;
         // a warp without rows only passes the barriers on (its rows of P and O are nobody's)
@@ -567,14 +567,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const bool in = R < p.geom.rows;
     const int b = in ? R / p.rows : 0, j = in ? R - b * p.rows : 0;
     const int hq = hk * p.G + j / p.q_len, i = j % p.q_len;
-    const bool takes = in && (int64_t)pd_length(p, __ldg(p.seq_lens + b)) - p.q_len >= (int64_t)p.geom.pages * 128;
     const int col = R / (2 * kSpRows), r = R % kSpRows;  // the same column and tile in all lanes
     const bool one = col >= p.geom.pairs;
     const int s0 = one ? 0 : R % (2 * kSpRows) / kSpRows;
     const int T = p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
     const int entries = one ? (p.geom.pages + 1) / 2 : p.geom.pages;
     wait_prerequisites();
-    const int used = __ldcg(p.split);
+    const int used = ld_cg(p.split);
+    const bool takes = in && (int64_t)pd_length(p, p.seq_lens[b]) - p.q_len >= (int64_t)p.geom.pages * 128;
     const int c0 = pd_holder(T, start, used), c1 = pd_holder(T, start + entries - 1, used);
     const int parts = (c1 - c0 + 1) * (one ? 2 : 1);
     const int64_t step = one ? 1 : 2;  // slots from a part to the next
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int64_t own = ((int64_t)b * p.Hkv + hk) * p.rows + j;
     float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     if (takes) {
-        const float2 last = __ldcg(reinterpret_cast<const float2*>(p.own_ml) + own);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
+        const float2 last = ld_cg(reinterpret_cast<const float2*>(p.own_ml) + own);
+        const float4 x = ld_cg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
         auto take = [&](float2 w, float4 y) {
             const float m = fmaxf(M, w.x), Mu = m == -INFINITY ? 0.f : m;
             const float f0 = ex2_approx(M - Mu), f = ex2_approx(w.x - Mu);
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         };
 #pragma unroll 8
         for (int k = 0; k < parts; ++k)
-            take(__ldcg(ml + k * step * kSpRows), __ldcg(po + k * step * (D / 4) * kSpRows));
+            take(ld_cg(ml + k * step * kSpRows), ld_cg(po + k * step * (D / 4) * kSpRows));
         take(last, x);
     }
     const bool some = L > 0.f && M != -INFINITY;
