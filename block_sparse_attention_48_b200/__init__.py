@@ -523,11 +523,12 @@ def _on_stream(fn):
 
 def paged_workspace(device: torch.device, need: int = 0) -> torch.Tensor:
     """The workspace paged_append, flex_decode_paged and flex_decode_shared use by
-    default: one per device and stream, zero-filled when allocated; a larger one takes
-    over its predecessor's status word (the predecessor is kept alive).  While a CUDA
-    graph is captured each call gets a workspace of the graph's own instead (pass ws= to
-    read the status of captured calls), of which every replay zeroes the status word and
-    the counters behind it."""
+    default: one per device and stream, its first 16 KB (the status word and counters)
+    zeroed when allocated; a larger one, at least twice as large, takes over its
+    predecessor's status word and replaces it.  While a CUDA graph is captured each call
+    gets a workspace of the graph's own instead (pass ws= to read the status of captured
+    calls), of which every replay zeroes the same 16 KB.  A capture that torch.cuda.graph
+    or CUDAGraph does not make has no memory of its own: pass ws= there."""
     return _binding.workspace(device.index if device.index is not None else torch.cuda.current_device(), need)
 
 

@@ -9,9 +9,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <algorithm>
 #include <map>
 #include <utility>
-#include <vector>
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -121,28 +121,33 @@ void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream(device).str
 constexpr int64_t kZeroed = 1 << 14;   // more than the status word and the counters
 constexpr int64_t kLeast = 1 << 22;
 
-// The workspace of the device's current stream, of at least `need` bytes: zero-filled
-// when allocated; a larger one takes over its predecessor's status word, and the
-// predecessor is kept.  While a graph is captured: one of the graph's own, whose start
-// every replay zeroes.
+// `size` bytes whose start, all that must have a value before a call, is zero.
+at::Tensor fresh_workspace(int device, int64_t size)
+{
+    at::Tensor ws = at::empty({size}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device));
+    ws.narrow(0, 0, kZeroed).zero_();
+    return ws;
+}
+
+// The workspace of the device's current stream, of at least `need` bytes.  A larger one takes
+// over its predecessor's status word and replaces it: the allocator reuses the memory in
+// the order of the stream, so calls under way keep theirs.  It is twice as large at least,
+// so that a batch that grows by and by allocates a few times only.  While a graph is
+// captured: one of the graph's own, whose start every replay zeroes.
 at::Tensor workspace(int device, int64_t need)
 {
-    const auto options = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device);
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
-        at::Tensor ws = at::empty({std::max(need, kZeroed)}, options);
-        ws.narrow(0, 0, kZeroed).zero_();
-        return ws;
-    }
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+        return fresh_workspace(device, std::max(need, kZeroed));
     // not destroyed at exit: the CUDA context may be gone by then
-    static auto* kept = new std::map<std::pair<int, void*>, std::vector<at::Tensor>>();
-    std::vector<at::Tensor>& mine = (*kept)[{device, stream_of(device)}];
-    if (mine.empty() || mine.back().numel() < need) {
-        at::Tensor ws = at::zeros({std::max(need, kLeast)}, options);
+    static auto* kept = new std::map<std::pair<int, void*>, at::Tensor>();
+    at::Tensor& mine = (*kept)[{device, stream_of(device)}];
+    if (!mine.defined() || mine.numel() < need) {
+        at::Tensor ws = fresh_workspace(device, std::max({need, kLeast, mine.defined() ? 2 * mine.numel() : 0}));
         const int64_t status = (int64_t)calls.workspace_size();
-        if (!mine.empty()) ws.narrow(0, 0, status).copy_(mine.back().narrow(0, 0, status));
-        mine.push_back(ws);
+        if (mine.defined()) ws.narrow(0, 0, status).copy_(mine.narrow(0, 0, status));
+        mine = ws;
     }
-    return mine.back();
+    return mine;
 }
 
 at::Tensor workspace_arg(PyObject* o, int device, int64_t need)
