@@ -256,6 +256,19 @@ PdLayout pd_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t pref
     return L;
 }
 
+// Head counts, rows and a prefix that the calls take: 0, or the status they are refused with.
+int check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D, int64_t prefix_pages)
+{
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    if (Hkv < 1 || Hq % Hkv != 0 || B > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+    const int64_t G = Hq / Hkv, most = fa::kPdMaxRows;
+    if (q_len > most || (q_len > 0 && G > most) || G * q_len > most) return FA_ERR_UNSUPPORTED;
+    const int64_t rows = G * q_len;
+    // the prefix's work list
+    if (B * rows > 0 && Hkv * (B * rows / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
 // Whether a shared prefix is taken once, by the kernel made for it, or page by page for
 // every sequence.  The first costs some 15 us more before it reads anything; the second
 // reads (B - 1) Hkv prefix_pages pages again, most of them from L2, and is slower the more a
@@ -297,13 +310,10 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if ((rc = check_tensor(q)) || (rc = check_tensor(o)) || (rc = check_pools(k_pages, v_pages))) return rc;
     const int64_t B = q->dims[0], Hq = q->dims[1], q_len = q->dims[2], D = q->dims[3];
     const int64_t Hkv = k_pages->dims[1], num_pages = k_pages->dims[0];
-    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
     if (!same_dims(q, o) || k_pages->dims[3] != D) return FA_ERR_INVALID_ARG;
-    if (Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-    if (B > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
     if (pages_per_seq < 0 || pages_per_seq > kMaxLen / FA_BLOCK_SIZE || page_table_stride < 0) return FA_ERR_INVALID_ARG;
     if (B > 1 && page_table_stride < pages_per_seq) return FA_ERR_INVALID_ARG;
-    if (q_len > fa::kPdMaxRows || (Hq / Hkv) * q_len > fa::kPdMaxRows) return FA_ERR_UNSUPPORTED;
+    if ((rc = check_shape(B, Hq, Hkv, q_len, D, prefix_pages)) != FA_OK) return rc;
     const int kind = sm ? sm->kind : FA_SCORE_NONE;
     if (kind < FA_SCORE_NONE || kind > FA_SCORE_BIAS_SOFTCAP) return FA_ERR_INVALID_ARG;
     if (kind == FA_SCORE_BIAS || kind == FA_SCORE_BIAS_SOFTCAP) return FA_ERR_UNSUPPORTED;
@@ -312,10 +322,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
     if (B * Hq * q_len == 0) return FA_OK;
     if (!seq_lens || (pages_per_seq > 0 && (!page_table || num_pages < 1))) return FA_ERR_INVALID_ARG;
-    // the kernels' work lists
-    if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;
-    if (prefix_pages > 0 && Hkv * (B * (Hq / Hkv) * q_len / (2 * fa::kSpRows) + 2) * prefix_pages > kMaxLen)
-        return FA_ERR_UNSUPPORTED;
+    if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;  // the work list
     const int64_t row0_pages = takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages) ? 0 : prefix_pages;
     if (row0_pages) prefix_pages = 0;
     const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
@@ -402,7 +409,7 @@ extern "C" {
 
 size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D)
 {
-    if (B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
+    if (B < 0 || Hq < 0 || q_len < 0 || check_shape(B, Hq, Hkv, q_len, D, 0) != FA_OK) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
     return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, 0).end;
 }
@@ -419,9 +426,10 @@ int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tenso
 size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
                                        int64_t prefix_len)
 {
-    if (prefix_len < 0 || prefix_len > kMaxLen || B < 0 || Hq < 0 || Hkv < 1 || q_len < 0 || D < 0) return 0;
-    if (B * Hq * q_len == 0) return kWorkspaceBytes;
+    if (prefix_len < 0 || prefix_len > kMaxLen || B < 0 || Hq < 0 || q_len < 0) return 0;
     const int64_t pages = prefix_len / FA_BLOCK_SIZE;
+    if (check_shape(B, Hq, Hkv, q_len, D, pages) != FA_OK) return 0;
+    if (B * Hq * q_len == 0) return kWorkspaceBytes;
     return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, pages) ? pages : 0).end;
 }
 

@@ -421,7 +421,7 @@ int fa_paged_append(const fa_tensor* k, const fa_tensor* v, const fa_tensor* q, 
 
 /* Bytes of device workspace fa_decode_paged needs (status word; counters and partial
  * results for every SM).  Does not depend on the batch or the cache's length, but on the
- * SM count of the current device. */
+ * SM count of the current device.  0 for a shape that the call refuses. */
 size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D);
 
 /* FlexDecoding over a paged cache: the forward pass for a few query tokens per
@@ -457,7 +457,7 @@ int fa_decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tenso
 
 /* Bytes of device workspace fa_decode_shared needs; where the prefix is taken once, it
  * grows with B * Hq * q_len (a partial result of every row and of every share of the
- * prefix). */
+ * prefix).  0 for a shape that the call refuses. */
 size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D,
                                        int64_t prefix_len);
 

@@ -1,4 +1,4 @@
-"""The serving calls' default workspaces: what is held as a batch grows."""
+"""The serving calls' default workspaces: what is held as a batch grows, and after refused calls."""
 
 import pytest
 import torch
@@ -53,3 +53,26 @@ def test_workspace_of_a_growing_batch():
         assert need(top) <= ws.numel()
         assert fa.device_status(ws=ws) == fa.FA_ERR_BAD_BLOCKMASK
         assert fa.device_status(ws=ws) == 0
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_refused_calls_get_no_workspace(shared):
+    """A call that is refused for its shape does not first take the memory that such a shape
+    would need, let alone keep it."""
+    fa = _fa()
+    pool = torch.zeros((3, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    lens = torch.full((1,), 200, dtype=torch.int32, device="cuda")
+    call = (lambda q: fa.flex_decode_shared(q, pool, pool, table, lens, PAGE)) if shared else \
+        (lambda q: fa.flex_decode_paged(q, pool, pool, table, lens))
+    for shape in ((1, 8, 1024, 64), (1, 4096, 1, 64)):
+        q = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            with pytest.raises(fa.FlexAttnError):
+                call(q)
+        assert _held(before) <= LEAST
+        # the outputs may have been made: of q's size and its rows in fp32
+        assert torch.cuda.max_memory_allocated() - before <= LEAST + 2 * q.numel() * 2 + 1024
