@@ -24,6 +24,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import inspect
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -510,12 +511,17 @@ def flex_attention_autograd(q, k, v, block_mask: BlockMask, score_mod=None, scal
 
 def _on_stream(fn):
     """Adds stream= to fn: the CUDA stream to run on (its own tensors are allocated for it)."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        if args[0].device != stream.device:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {args[0].device}")
+        tensor = args[0] if args else kw.get(first)
+        if not isinstance(tensor, torch.Tensor):
+            raise TypeError(f"{fn.__name__}: {first}: expected a tensor, got {type(tensor).__name__}")
+        if tensor.device != stream.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {tensor.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call
