@@ -93,6 +93,13 @@ at::Tensor readable(const at::Tensor& t)
     return ok ? t : t.is_contiguous() ? t.clone() : t.contiguous();
 }
 
+// A tensor of the caller's has been written: autograd's count of its changes in place goes up,
+// as after torch's own in-place operators (a tensor made in inference mode has none).
+void written(const at::Tensor& t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Data of an int32 tensor of one or two dimensions (a size of -1: any), the last contiguous.
 const int32_t* ints(const at::Tensor& t, int dims, int64_t n0, int64_t n1, int device, const char* what)
 {
@@ -237,6 +244,8 @@ PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int rc = calls.rope_apply(&qd, has_k ? &kd : nullptr, &rope, pos, stride, integer(a[7]), truth(a[6]) ? 1 : 0, &qo,
                                     has_k ? &ko : nullptr, stream_of(device));
     if (rc) return PyLong_FromLong(rc);
+    if (a[8] != Py_None) written(q_out);
+    if (a[9] != Py_None) written(k_out);
     return pair(THPVariable_Wrap(q_out), has_k ? THPVariable_Wrap(k_out) : none());
     END_HANDLE_TH_ERRORS
 }
@@ -252,8 +261,8 @@ PyObject* py_paged_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     const at::Tensor k = readable(k0), v = readable(tensor(a[1], "v"));
     const fa_tensor kd = describe(k, device, "k"), vd = describe(v, device, "v");
-    const fa_tensor kp = describe(tensor(a[2], "k_pages"), device, "k_pages");
-    const fa_tensor vp = describe(tensor(a[3], "v_pages"), device, "v_pages");
+    const at::Tensor &k_pages = tensor(a[2], "k_pages"), &v_pages = tensor(a[3], "v_pages");
+    const fa_tensor kp = describe(k_pages, device, "k_pages"), vp = describe(v_pages, device, "v_pages");
     const int64_t B = k.size(0);
     const at::Tensor& table = tensor(a[4], "page_table");
     const int32_t* pages = ints(table, 2, B, -1, device, "page_table");
@@ -276,6 +285,9 @@ PyObject* py_paged_append(PyObject*, PyObject* const* a, Py_ssize_t n)
                                       table.stride(0), table.size(1), &kp, &vp, has_q ? &qo : nullptr, ws.data_ptr(),
                                       (size_t)ws.numel(), stream_of(device));
     if (rc) return PyLong_FromLong(rc);
+    written(k_pages);
+    written(v_pages);
+    if (a[8] != Py_None) written(q_out);
     return has_q ? THPVariable_Wrap(q_out) : none();
     END_HANDLE_TH_ERRORS
 }
@@ -327,6 +339,8 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
         &qd, &kp, &vp, pages, table.stride(0), table.size(1), lens, extra, &sm, (float)number(a[10]), &od,
         lse.data_ptr<float>(), ws.data_ptr(), (size_t)ws.numel(), stream_of(device));
     if (rc) return PyLong_FromLong(rc);
+    if (a[11] != Py_None) written(out);
+    if (a[12] != Py_None) written(lse);
     return pair(THPVariable_Wrap(out), THPVariable_Wrap(lse));
     END_HANDLE_TH_ERRORS
 }
