@@ -117,7 +117,8 @@ fa_rope rope_of(const at::Tensor& f, bool interleaved, double amplitude, int dev
     TORCH_CHECK_TYPE(f.scalar_type() == at::kDouble && f.dim() == 1 && f.is_cuda() && f.get_device() == device &&
                          (f.size(0) <= 1 || f.stride(0) == 1),
                      "inv_freq: expected a contiguous fp64 tensor [rotary_dim / 2] on cuda:", device);
-    TORCH_CHECK_VALUE(amplitude > 0, "amplitude must be positive");
+    // in fp32, where 0 would mean 1 to the C ABI
+    TORCH_CHECK_VALUE((float)amplitude > 0.f, "amplitude must be positive (in fp32)");
     return {f.data_ptr<double>(), (int32_t)(2 * f.size(0)), interleaved ? 1 : 0, (float)amplitude};
 }
 

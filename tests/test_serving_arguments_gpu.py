@@ -55,3 +55,15 @@ def test_tensors_written_in_place_are_marked():
     fa.paged_append(new, new, k2, k2.clone(), table, sl - 1)
     fa.flex_decode_paged(q, k, v, table, sl, out=out2)
     assert torch.equal(out2, out)
+
+
+def test_an_amplitude_that_fp32_rounds_to_zero_is_refused():
+    """An amplitude of 0 means 1 to the C ABI: what becomes 0 in fp32 must not turn into it."""
+    fa = _fa()
+    f = torch.ones(32, dtype=torch.float64, device="cuda")
+    q = torch.ones((1, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    for amp in (1e-50, 0.0, -1.0, float("nan")):
+        with pytest.raises(ValueError):
+            fa.rope_apply(q, None, f, amplitude=amp)
+    small = fa.rope_apply(q, None, f, amplitude=1e-30)[0]
+    assert float(small.abs().max()) < 2e-30
