@@ -318,7 +318,11 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (kind < FA_SCORE_NONE || kind > FA_SCORE_BIAS_SOFTCAP) return FA_ERR_INVALID_ARG;
     if (kind == FA_SCORE_BIAS || kind == FA_SCORE_BIAS_SOFTCAP) return FA_ERR_UNSUPPORTED;
     if (kind == FA_SCORE_ALIBI && !sm->alibi_slopes) return FA_ERR_INVALID_ARG;
-    if (kind == FA_SCORE_SOFTCAP && !(sm->softcap > 0.f)) return FA_ERR_INVALID_ARG;
+    const float factor = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
+    // cap tanh(s / cap) with the cap and its inverse taken into the scores' factors
+    if (kind == FA_SCORE_SOFTCAP &&
+        (!(sm->softcap > 0.f) || !std::isfinite(factor / sm->softcap) || !std::isfinite(sm->softcap * 1.5f)))
+        return FA_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
     if (B * Hq * q_len == 0) return FA_OK;
     if (!seq_lens || (pages_per_seq > 0 && (!page_table || num_pages < 1))) return FA_ERR_INVALID_ARG;
@@ -353,7 +357,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.row0_pages = (int32_t)row0_pages;
     P.has_window = window >= 0 ? 1 : 0;
     P.window = window >= 0 ? (window < kMaxLen ? window : kMaxLen) : 0;
-    P.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
+    P.scale = factor;
     if (kind == FA_SCORE_SOFTCAP) {
         P.softcap = sm->softcap;
         P.softcap_in = P.scale / sm->softcap;

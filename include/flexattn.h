@@ -437,8 +437,9 @@ size_t fa_decode_paged_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_
  *      Pages may be shared between sequences.  Whatever the places behind a sequence's
  *      last key, or keys a row does not attend, hold (infinities and NaN included) does
  *      not reach the row.
- *      window < 0: none.  sm: NONE, ALIBI or SOFTCAP (NULL = none); ALiBi's distance is
- *      that of the positions.  scale as fa_forward.
+ *      window < 0: none.  sm: NONE, ALIBI or SOFTCAP (NULL = none; a cap for which
+ *      1.5 cap and scale / cap are finite in fp32); ALiBi's distance is that of the
+ *      positions.  scale as fa_forward.
  *      workspace: >= fa_decode_paged_workspace_size(...) bytes, 16-byte aligned, its
  *      first 16 KB zeroed once before its first use; every call leaves it ready for the
  *      next, of any shape (after FA_ERR_TIMEOUT zero it again).  Calls that overlap in

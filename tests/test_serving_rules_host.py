@@ -1,4 +1,7 @@
-"""The serving calls' rules that need no GPU: what a workspace is sized for."""
+"""The serving calls' rules that need no GPU: what a workspace is sized for, and soft caps
+that fp32 cannot work with."""
+
+import math
 
 import pytest
 
@@ -28,3 +31,27 @@ def test_workspaces_of_taken_shapes():
         assert lib.fa_decode_shared_workspace_size(B, Hq, 2, n, 64, 2 ** 31 - 256) == 256
     # a prefix's work list of 2^31 entries is refused
     assert lib.fa_decode_shared_workspace_size(65535, 16, 1, 1, 64, 2 ** 31 - 256) == 0
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_soft_caps_beyond_fp32_are_refused(shared):
+    """The kernels multiply by scale / cap and by cap log2(e): both must be finite, or every
+    output would be NaN."""
+    lib = fa.library()
+
+    def tensor(dims, data=4096):
+        t = fa.TensorDesc()
+        t.data = data
+        for i in range(4):
+            t.dims[i], t.strides[i] = dims[i], math.prod(dims[i + 1:])
+        return t
+    q, pool = tensor([2, 8, 1, 64]), tensor([5, 2, 128, 64])
+    sm = fa.ScoreModDesc()
+    sm.kind = fa.SCORE["softcap"]
+
+    def call(cap, scale):
+        sm.softcap = cap
+        fn = lib.fa_decode_shared if shared else lib.fa_decode_paged
+        return fn(q, pool, pool, 4096, 3, 3, 4096, 128 if shared else -1, sm, scale, q, None, 4096, 1 << 30, None)
+    for cap, scale in ((math.inf, 0.0), (math.nan, 0.0), (3e38, 0.0), (1e-40, 0.0), (1e-30, 1e10), (-1.0, 0.0)):
+        assert call(cap, scale) == fa.FA_ERR_INVALID_ARG
