@@ -145,7 +145,14 @@ def _load():
 _lib = _load()
 if not os.path.exists(os.path.join(_HERE, "_binding.so")):
     raise ImportError("_binding.so is missing: build it with `python block_sparse_attention_48_b200/build.py`")
-from . import _binding  # noqa: E402  (the serving calls' binding; needs torch loaded)
+try:
+    from . import _binding  # noqa: E402  (the serving calls' binding; needs torch loaded)
+except ImportError as e:
+    raise ImportError("_binding.so does not load, as after a change of torch or Python: build it again with "
+                      "`python block_sparse_attention_48_b200/build.py`") from e
+if _binding.torch_version != torch.__version__:
+    raise ImportError(f"_binding.so was built against torch {_binding.torch_version}, this is {torch.__version__}: build "
+                      "it again with `python block_sparse_attention_48_b200/build.py`")
 
 _binding.bind(*[ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
                 ("fa_rope_apply", "fa_paged_append", "fa_decode_paged", "fa_decode_shared",

@@ -13,6 +13,7 @@ import concurrent.futures
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -51,19 +52,35 @@ def _older(target: str, deps) -> bool:
     return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
 
 
+def _torch() -> tuple:
+    """(directory, version) of the installed torch, without importing it."""
+    where = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(where, "version.py")) as f:
+        return where, re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read()).group(1)
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile _binding.so (no CUDA code; torch is found without importing it)."""
+    """Compile _binding.so (no CUDA code).  It is good for the torch and the Python that it
+    was built against, which _build/_binding.for names."""
+    torch_dir, version = _torch()
+    built_for, record = f"torch {version}, {sysconfig.get_config_var('SOABI')}", os.path.join(BUILD_DIR, "_binding.for")
     if not force and not _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
-        return BINDING
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        if os.path.exists(record):
+            with open(record) as f:
+                if f.read() == built_for:
+                    return BINDING
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = BINDING + f".tmp{os.getpid()}"
-    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc,
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f'-DFA_TORCH_VERSION="{version}"',
+                           "-I", INCLUDE, "-isystem", inc,
                            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
                            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
                            BINDING_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(record, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

@@ -4,6 +4,9 @@
 // call, here 5 to 8.  The C ABI's functions come in as addresses (bind), so that this
 // file needs no link against the CUDA library.
 //
+// It is compiled against one torch (FA_TORCH_VERSION, the build's), which the package checks
+// when it is imported.
+//
 // Every function takes positional arguments and returns its outputs, or the fa_status of
 // a call that the library refused.
 #define PY_SSIZE_T_CLEAN
@@ -365,5 +368,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 PyMODINIT_FUNC PyInit__binding()
 {
-    return PyModule_Create(&module);
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", FA_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }
