@@ -4,9 +4,10 @@
 // latency, and the start of CTAs on SMs that the previous kernel has left.
 //
 // What the previous kernel writes is then written while this one is already running.  So
-// such a kernel loads with ordinary loads, or ld_cg: the read-only path (__ldg, ld.global.nc)
-// is for memory that nothing writes in a kernel's whole lifetime, and the compiler may move
-// such loads, and the other __ld functions, over the wait.
+// such a kernel loads with ordinary loads, which are coherent and stay behind the wait: the
+// read-only path (__ldg, ld.global.nc) is for memory that nothing writes in a kernel's whole
+// lifetime, and the compiler may move such loads, and those of the other __ld functions, over
+// the wait.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,32 +24,6 @@ __device__ __forceinline__ void launch_dependents()
 __device__ __forceinline__ void wait_prerequisites()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// Loads from L2, issued where they stand: of what other CTAs of this kernel, or the kernel
-// before, have written.
-__device__ __forceinline__ int ld_cg(const int* p)
-{
-    int x;
-    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
-    return x;
-}
-
-__device__ __forceinline__ float2 ld_cg(const float2* p)
-{
-    float2 x;
-    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(p) : "memory");
-    return x;
-}
-
-__device__ __forceinline__ float4 ld_cg(const float4* p)
-{
-    float4 x;
-    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                 : "l"(p)
-                 : "memory");
-    return x;
 }
 
 template <class... P>

