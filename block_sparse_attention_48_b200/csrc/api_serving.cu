@@ -12,6 +12,7 @@
 #include "flexattn.h"
 #include "paged_decode.cuh"
 #include "rope.cuh"
+#include "serving_rules.h"
 #include "shared_prefix.cuh"
 
 using fa::aligned16;
@@ -269,37 +270,6 @@ int check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t q_len, int64_t D, in
     return FA_OK;
 }
 
-// Whether a shared prefix is taken once, by the kernel made for it, or page by page for
-// every sequence.  The first costs some 15 us more before it reads anything; the second
-// reads (B - 1) Hkv prefix_pages pages again, most of them from L2, and is slower the more a
-// page costs it.  Page by page / once, us on a B200: to 8 rows, D 128, 21.3 / 24.3 at 1976
-// such pages, 30.3 / 30.4 at 3952, 33.8 / 31.0 at 4096; D 64, 24.8 / 28.6 at 3952, 30.5 / 30.1
-// at 6016; to 16 rows, D 128, 33.0 / 25.7 at 896, 41.1 / 34.8 at 1976; D 64, 26.2 / 28.1 at
-// 1976, 36.1 / 29.8 at 3952.
-bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
-{
-    const int64_t least = D == 128 ? (rows > 8 ? 1024 : 4096) : rows > 8 ? 2048 : 6144;
-    return (B - 1) * Hkv * prefix_pages >= least;
-}
-
-// Teams for `segments` segments of at most `pages` pages: all `most` of them, unless few
-// segments would be cut into more pieces than pay.  With n teams a team takes about T / n us
-// for T pages, and a segment's last team `cost` ns for each of its n / segments pieces: the
-// sum is least at n^2 = 1000 T segments / cost.  The pieces are then of whole pages and as
-// many for every segment, so that no share runs over two segments of equal length.  All / the
-// fewer teams, us on a B200: one segment of 30000 keys (8 rows, D 128) 60.1 / 22.3; 2 of 8000 (4
-// rows, D 64) 14.8 / 11.2; 2 of 60000 (16 rows, D 128) 52.0 / 34.8; 8 of 8000 (16 rows, D 128)
-// 26.7 / 22.0; 9 of 3746 to 4998 (4 rows, D 64) 14.2 / 15.3.  (By the page table's width: a
-// rule on the lengths themselves, on the device, cost every call 0.3 us.)
-int32_t teams_that_pay(int64_t segments, int64_t pages, int64_t rows, int64_t D, int64_t most)
-{
-    const double cost = rows > 8 ? 50.0 * (double)D / 64 : 45.0 * (double)((rows * D + 511) / 512);
-    const double pieces = std::sqrt(1000.0 * (double)pages / cost);  // of a segment
-    if (!(pieces * (double)segments < (double)most) || pieces >= (double)pages) return (int32_t)most;
-    const int64_t m = pieces < 1.0 ? 1 : (int64_t)pieces, share = (pages + m - 1) / m;
-    return (int32_t)(segments * ((pages + share - 1) / share));
-}
-
 // fa_decode_paged and fa_decode_shared (prefix_len > 0).
 int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages, const int32_t* page_table,
                  int64_t page_table_stride, int64_t pages_per_seq, const int32_t* seq_lens, int64_t window,
@@ -327,7 +297,7 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     if (B * Hq * q_len == 0) return FA_OK;
     if (!seq_lens || (pages_per_seq > 0 && (!page_table || num_pages < 1))) return FA_ERR_INVALID_ARG;
     if (B * Hkv * pages_per_seq > kMaxLen) return FA_ERR_UNSUPPORTED;  // the work list
-    const int64_t row0_pages = takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages) ? 0 : prefix_pages;
+    const int64_t row0_pages = fa::takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages) ? 0 : prefix_pages;
     if (row0_pages) prefix_pages = 0;
     const PdLayout lay = pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, prefix_pages);
     if (lay.sms <= 0) return FA_ERR_CUDA;
@@ -365,7 +335,8 @@ int decode_paged(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* 
     P.slopes = kind == FA_SCORE_ALIBI ? sm->alibi_slopes : nullptr;
     const int64_t most = B * Hkv * pages_per_seq;  // one CTA per SM, never more than pages in all
     P.grid = (int32_t)(most < 1 ? 1 : most < lay.sms ? most : lay.sms);
-    P.teams = teams_that_pay(B * Hkv, pages_per_seq, P.rows, D, lay.sms * fa::kPdTeams);
+    P.teams = fa::teams_that_pay(B * Hkv, fa::pages_of_a_segment(pages_per_seq, window, q_len), P.rows, D,
+                                 lay.sms * fa::kPdTeams);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.arrived = reinterpret_cast<unsigned*>(ws + lay.arrived);
     P.part_ml = reinterpret_cast<float*>(ws + lay.ml);
@@ -434,7 +405,7 @@ size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64
     const int64_t pages = prefix_len / FA_BLOCK_SIZE;
     if (check_shape(B, Hq, Hkv, q_len, D, pages) != FA_OK) return 0;
     if (B * Hq * q_len == 0) return kWorkspaceBytes;
-    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, pages) ? pages : 0).end;
+    return pd_layout(B, Hkv, (Hq / Hkv) * q_len, D, fa::takes_prefix_once(B, Hkv, (Hq / Hkv) * q_len, D, pages) ? pages : 0).end;
 }
 
 int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,

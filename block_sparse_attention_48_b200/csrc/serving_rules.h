@@ -1,0 +1,54 @@
+// The serving calls' choices between ways of one result, by sizes (also built for the unit
+// tests).
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+namespace fa {
+
+// Whether a shared prefix is taken once, by the kernel made for it, or page by page for
+// every sequence.  The first costs some 15 us more before it reads anything; the second
+// reads (B - 1) Hkv prefix_pages pages again, most of them from L2, and is slower the more a
+// page costs it.  Page by page / once, us on a B200: to 8 rows, D 128, 21.3 / 24.3 at 1976
+// such pages, 30.3 / 30.4 at 3952, 33.8 / 31.0 at 4096; D 64, 24.8 / 28.6 at 3952, 30.5 / 30.1
+// at 6016; to 16 rows, D 128, 33.0 / 25.7 at 896, 41.1 / 34.8 at 1976; D 64, 26.2 / 28.1 at
+// 1976, 36.1 / 29.8 at 3952.
+inline bool takes_prefix_once(int64_t B, int64_t Hkv, int64_t rows, int64_t D, int64_t prefix_pages)
+{
+    const int64_t least = D == 128 ? (rows > 8 ? 1024 : 4096) : rows > 8 ? 2048 : 6144;
+    return (B - 1) * Hkv * prefix_pages >= least;
+}
+
+// Pages that a segment can have: those of the table, or that a window of `window` keys before
+// the first of q_len query tokens reaches (window < 0: none).  Teams by the table alone / by
+// this, us on a B200, 600 pages of table and a window of 16384: one sequence, 16 rows, D 128
+// 27.8 / 23.8; 4 sequences, 8 rows, D 128 32.3 / 21.3; 2 of 4 rows, D 64 20.6 / 14.9.  (Behind a
+// prefix that is taken once the table's width is kept: without the prefix's pages it made no
+// difference, 102.8 / 102.9 and 95.3 / 95.7.)
+inline int64_t pages_of_a_segment(int64_t pages_per_seq, int64_t window, int64_t q_len)
+{
+    if (window < 0 || window >= 128 * pages_per_seq) return pages_per_seq;
+    const int64_t reach = (window + q_len + 126) / 128 + 1;
+    return reach < pages_per_seq ? reach : pages_per_seq;
+}
+
+// Teams for `segments` segments of at most `pages` pages: all `most` of them, unless few
+// segments would be cut into more pieces than pay.  With n teams a team takes about T / n us
+// for T pages, and a segment's last team `cost` ns for each of its n / segments pieces: the
+// sum is least at n^2 = 1000 T segments / cost.  The pieces are then of whole pages and as
+// many for every segment, so that no share runs over two segments of equal length.  All / the
+// fewer teams, us on a B200: one segment of 30000 keys (8 rows, D 128) 60.1 / 22.3; 2 of 8000 (4
+// rows, D 64) 14.8 / 11.2; 2 of 60000 (16 rows, D 128) 52.0 / 34.8; 8 of 8000 (16 rows, D 128)
+// 26.7 / 22.0; 9 of 3746 to 4998 (4 rows, D 64) 14.2 / 15.3.  (By the page table's width: a
+// rule on the lengths themselves, on the device, cost every call 0.3 us.)
+inline int32_t teams_that_pay(int64_t segments, int64_t pages, int64_t rows, int64_t D, int64_t most)
+{
+    const double cost = rows > 8 ? 50.0 * (double)D / 64 : 45.0 * (double)((rows * D + 511) / 512);
+    const double pieces = std::sqrt(1000.0 * (double)pages / cost);  // of a segment
+    if (!(pieces * (double)segments < (double)most) || pieces >= (double)pages) return (int32_t)most;
+    const int64_t m = pieces < 1.0 ? 1 : (int64_t)pieces, share = (pages + m - 1) / m;
+    return (int32_t)(segments * ((pages + share - 1) / share));
+}
+
+} // namespace fa

@@ -1,5 +1,5 @@
-"""Decoding behind a shared prefix that is taken once: lengths out of range, and long
-lists with an odd number of shared pages."""
+"""Decoding with lengths that the other tests do not have: out of range behind a shared prefix
+that is taken once, and few long sequences with a window or of unequal lengths."""
 
 import pytest
 import torch
@@ -41,3 +41,31 @@ def test_shared_prefix_once_with_bad_lengths(kind):
     got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), prefix, score_mod=on_gpu, ws=ws)
     assert fa.device_status(ws=ws) == fa.FA_ERR_BAD_BLOCKMASK
     assert_decode(got, decode_ref(q, k, v, table, lens, None, score))
+
+
+@pytest.mark.parametrize("case", [
+    # lens, q_len, Hq, Hkv, D, window, score
+    ([30000], 1, 16, 1, 128, 16384, None),
+    ([20000, 3000, 9100], 2, 8, 1, 128, 4096, "softcap"),
+    ([25000, 14], 5, 6, 2, 64, 9000, None),
+    ([1200, 2500, 1700, 2111, 1500], 1, 16, 1, 128, None, None),
+    ([2000, 5700, 130, 4100], 2, 4, 2, 64, None, "softcap"),
+    ([2500, 2500, 2500], 1, 8, 1, 128, None, None),
+], ids=lambda c: "-".join(str(x) for x in c)[:60])
+def test_decode_of_few_segments(case):
+    """Few segments, alike and not, with a window and without: right whatever the number of
+    teams that take them, and the same bits every time; tables of just the pages and much
+    wider ones."""
+    fa = _fa()
+    lens, n, Hq, Hkv, D, window, kind = case
+    score = ("softcap", 5.0) if kind else None
+    for width in (None, 3 * ((max(lens) + PAGE - 1) // PAGE)):
+        q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=len(lens) + D, width=width, filler=float("nan"))
+        args = [t.cuda() for t in (q, k, v, table, sl)]
+        ws = torch.zeros(1 << 23, dtype=torch.uint8, device="cuda")
+        got = fa.flex_decode_paged(*args, window=window, score_mod=score, ws=ws)
+        assert_decode(got, decode_ref(q, k, v, table, lens, window, score))
+        for _ in range(5):
+            again = fa.flex_decode_paged(*args, window=window, score_mod=score, ws=ws)
+            assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+        assert fa.device_status(ws=ws) == 0

@@ -1,11 +1,32 @@
-"""The serving calls' rules that need no GPU: what a workspace is sized for, and soft caps
-that fp32 cannot work with."""
+"""The serving calls' rules that need no GPU: what a workspace is sized for, soft caps that
+fp32 cannot work with, and how many teams a call gets (csrc/serving_rules.h, built for the
+host)."""
 
+import ctypes
 import math
+import os
+import random
+import subprocess
 
 import pytest
 
 import block_sparse_attention_48_b200 as fa
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BUILD = os.path.join(ROOT, "tests", "host", "_build")
+
+
+@pytest.fixture(scope="module")
+def rules():
+    os.makedirs(BUILD, exist_ok=True)
+    out = os.path.join(BUILD, "libservingrules.so")
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I",
+                           os.path.join(ROOT, "block_sparse_attention_48_b200", "csrc"),
+                           os.path.join(ROOT, "tests", "host", "serving_rules.cpp"), "-o", out])
+    L, i64 = ctypes.CDLL(out), ctypes.c_int64
+    L.fa_host_segment_pages.argtypes, L.fa_host_segment_pages.restype = [i64] * 3, i64
+    L.fa_host_teams.argtypes = L.fa_host_once.argtypes = [i64] * 5
+    return L
 
 
 @pytest.mark.parametrize("shape", [
@@ -55,3 +76,35 @@ def test_soft_caps_beyond_fp32_are_refused(shared):
         return fn(q, pool, pool, 4096, 3, 3, 4096, 128 if shared else -1, sm, scale, q, None, 4096, 1 << 30, None)
     for cap, scale in ((math.inf, 0.0), (math.nan, 0.0), (3e38, 0.0), (1e-40, 0.0), (1e-30, 1e10), (-1.0, 0.0)):
         assert call(cap, scale) == fa.FA_ERR_INVALID_ARG
+
+
+def test_pages_of_a_segment(rules):
+    """No segment has more pages than the rule says, and some segment has as many: by the
+    pages that the keys of a window touch, at every length."""
+    rng = random.Random(5)
+    for _ in range(300):
+        width, n = rng.randint(0, 40), rng.randint(1, 16)
+        window = rng.choice([-1, 0, 1, 126, 127, 128, 129, 500, rng.randint(0, 6000), 2 ** 62])
+        most = 0
+        for length in range(0, 128 * width + 1):
+            first = length - n - window if 0 <= window and length - n > window else 0
+            most = max(most, (length + 127) // 128 - first // 128)
+        got = rules.fa_host_segment_pages(width, window, n)
+        assert got == most, (width, window, n)
+
+
+def test_teams_that_pay(rules):
+    """All teams, or as many for every segment, each with a whole page at least; a window's
+    segments count as what they read."""
+    rng = random.Random(6)
+    for _ in range(3000):
+        segments, pages = rng.choice([1, 2, 3, 8, 9, 40, 600]), rng.randint(0, 4000)
+        rows, D, most = rng.randint(1, 16), rng.choice([64, 128]), rng.choice([2, 296])
+        n = rules.fa_host_teams(segments, pages, rows, D, most)
+        assert n == most or (n % segments == 0 and segments <= n < most and n // segments <= pages)
+    # one sequence behind a window: as with a table of the pages that it reads
+    reads = rules.fa_host_segment_pages(600, 16384, 1)
+    assert reads == 129
+    for rows in (4, 8, 16):
+        n = rules.fa_host_teams(1, reads, rows, 128, 296)
+        assert n <= reads // 2 and n < rules.fa_host_teams(1, 600, rows, 128, 296)
