@@ -44,6 +44,33 @@ def test_shared_prefix_once_with_bad_lengths(kind):
 
 
 @pytest.mark.parametrize("case", [
+    # batch, own lengths (cycled), prefix pages, q_len, Hq, Hkv, score
+    (33, (1, 130, 7), 8, 1, 16, 1, None),
+    (12, (40, 300, 129, 4), 6, 4, 16, 4, "softcap"),
+    (20, (5, 2000), 14, 5, 6, 2, "alibi"),
+], ids=lambda c: f"b{c[0]}-p{c[2]}-n{c[3]}-h{c[4]}-{c[5]}-{c[6]}")
+def test_shared_prefix_once_of_few_pages(case):
+    """More than eight rows per kv head, D = 128, behind a short prefix."""
+    fa = _fa()
+    B, own, pages, n, Hq, Hkv, kind = case
+    prefix = PAGE * pages
+    lens = [prefix + own[i % len(own)] for i in range(B)]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, 128, seed=B, prefix=prefix, filler=float("nan"))
+    _assert_taken_once(fa, q, k, prefix)
+    slopes = torch.tensor([2.0 ** (-8 * (h + 1) / Hq) for h in range(Hq)], dtype=torch.float32)
+    score = {None: None, "alibi": ("alibi", slopes), "softcap": ("softcap", 5.0)}[kind]
+    args = [t.cuda() for t in (q, k, v, table, sl)]
+    kw = dict(score_mod=("alibi", slopes.cuda()) if kind == "alibi" else score,
+              ws=torch.zeros(1 << 25, dtype=torch.uint8, device="cuda"))
+    got = fa.flex_decode_shared(*args, prefix, **kw)
+    assert_decode(got, decode_ref(q, k, v, table, lens, None, score))
+    for _ in range(5):
+        again = fa.flex_decode_shared(*args, prefix, **kw)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert fa.device_status(ws=kw["ws"]) == 0
+
+
+@pytest.mark.parametrize("case", [
     # lens, q_len, Hq, Hkv, D, window, score
     ([30000], 1, 16, 1, 128, 16384, None),
     ([20000, 3000, 9100], 2, 8, 1, 128, 4096, "softcap"),

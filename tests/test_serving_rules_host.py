@@ -108,3 +108,26 @@ def test_teams_that_pay(rules):
     for rows in (4, 8, 16):
         n = rules.fa_host_teams(1, reads, rows, 128, 296)
         assert n <= reads // 2 and n < rules.fa_host_teams(1, 600, rows, 128, 296)
+
+
+def test_where_a_prefix_is_taken_once(rules):
+    """By the pages that would be read again: more of them, of any of the sizes, never turn it
+    back; both sides of each threshold."""
+    def once(B, Hkv, rows, D, pages):
+        return bool(rules.fa_host_once(B, Hkv, rows, D, pages))
+    for B, Hkv, rows, D, least in ((33, 1, 8, 128, 4096), (33, 1, 8, 64, 6144), (33, 1, 4, 64, 6144), (33, 1, 9, 64, 2048),
+                                   (33, 1, 16, 128, 256), (13, 1, 16, 128, 256), (11, 1, 16, 128, 1024),
+                                   (3, 8, 16, 128, 1024)):
+        pages = -(-least // ((B - 1) * Hkv))
+        assert once(B, Hkv, rows, D, pages) and not once(B, Hkv, rows, D, pages - 1), (B, rows, D)
+    assert not once(65, 2, 16, 128, 4) and once(65, 2, 16, 128, 5)  # 512 and 640 pages
+    assert not once(2, 8, 16, 128, 10 ** 4) and once(2, 8, 16, 64, 10 ** 4)
+    assert not any(once(1, 8, r, D, 10 ** 5) or once(9, 8, r, D, 0) for r in (1, 16) for D in (64, 128))
+    rng = random.Random(8)
+    for _ in range(2000):
+        x = [rng.randint(3, 200), rng.randint(1, 16), rng.randint(1, 16), rng.choice([64, 128]), rng.randint(1, 300)]
+        if once(*x):
+            for i in (0, 1, 4):
+                y = list(x)
+                y[i] += rng.randint(1, 50)
+                assert once(*y)
