@@ -96,3 +96,24 @@ def test_decode_of_few_segments(case):
             again = fa.flex_decode_paged(*args, window=window, score_mod=score, ws=ws)
             assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
         assert fa.device_status(ws=ws) == 0
+
+
+@pytest.mark.parametrize("shape", [(3, 8, 8, 128, 1), (4, 8, 8, 64, 2), (3, 32, 8, 128, 4)])
+def test_shared_prefix_once_over_long_lists(shape):
+    """Few sequences behind an odd number of shared pages, taken once, and shares of 20 and
+    more own pages that run over several segments; calls one after another give the same
+    bits."""
+    fa = _fa()
+    B, Hq, Hkv, D, n = shape
+    prefix = 301 * PAGE
+    lens = [prefix + (11000, 300, 4001, 2 * n)[i] for i in range(B)]
+    q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=79, prefix=prefix, filler=float("nan"))
+    _assert_taken_once(fa, q, k, prefix)
+    args = [t.cuda() for t in (q, k, v, table, sl)]
+    ws = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+    got = fa.flex_decode_shared(*args, prefix, ws=ws)
+    assert_decode(got, decode_ref(q, k, v, table, lens))
+    for _ in range(20):
+        again = fa.flex_decode_shared(*args, prefix, ws=ws)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert fa.device_status(ws=ws) == 0
