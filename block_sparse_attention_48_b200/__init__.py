@@ -658,7 +658,9 @@ def flex_decode_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
                        ws: Optional[torch.Tensor] = None):
     """flex_decode_paged for sequences that share their first prefix_len keys (a multiple
     of 128: the first prefix_len / 128 entries of every row of page_table are the same
-    pages), which are taken once for the whole batch (fa_decode_shared)."""
+    pages), which are taken once for the whole batch (fa_decode_shared).  They are read from
+    row 0, whatever sequence 0's length; a sequence that ends in the prefix is taken from its
+    own row."""
     r = _binding.decode(True, q, k_pages, v_pages, page_table, seq_lens, prefix_len, *_score(score_mod),
                         0.0 if scale is None else scale, out, lse, ws)
     return r if r.__class__ is tuple else _check(r, "fa_decode_shared")

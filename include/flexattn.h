@@ -470,8 +470,9 @@ size_t fa_decode_shared_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64
  *
  * In:  as fa_decode_paged; prefix_len >= 0, a multiple of FA_BLOCK_SIZE, at most
  *      pages_per_seq * FA_BLOCK_SIZE.  The shared entries are read from row 0 for the
- *      sequences whose every query token sits at position >= prefix_len; a shorter
- *      sequence is taken by itself from its own row.
+ *      sequences whose every query token sits at position >= prefix_len, so row 0 names
+ *      them even where sequence 0 itself is shorter or empty; a shorter sequence is taken
+ *      by itself from its own row.
  * Errors: as fa_decode_paged; FA_ERR_INVALID_ARG for such a prefix_len. */
 int fa_decode_shared(const fa_tensor* q, const fa_tensor* k_pages, const fa_tensor* v_pages,
                      const int32_t* page_table, int64_t page_table_stride, int64_t pages_per_seq,

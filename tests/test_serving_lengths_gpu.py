@@ -117,3 +117,23 @@ def test_shared_prefix_once_over_long_lists(shape):
         again = fa.flex_decode_shared(*args, prefix, ws=ws)
         assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
     assert fa.device_status(ws=ws) == 0
+
+
+@pytest.mark.parametrize("B", [6, 40])
+def test_shared_prefix_with_an_empty_first_sequence(B):
+    """Sequence 0 empty, or ending in the prefix: its row still names the shared pages, and the
+    others read them there (page by page and taken once)."""
+    fa = _fa()
+    pages, n, Hq, Hkv, D = 30, 1, 8, 4, 128
+    prefix = PAGE * pages
+    for first in (0, 200):
+        lens = [first] + [prefix + 5 + 31 * i for i in range(1, B)]
+        q, k, v, table, sl = paged_case(lens, n, Hq, Hkv, D, seed=B, prefix=prefix, filler=float("nan"))
+        if B == 40:
+            _assert_taken_once(fa, q, k, prefix)
+        tab = table.clone()
+        tab[1:, :pages] = -1
+        ws = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+        got = fa.flex_decode_shared(q.cuda(), k.cuda(), v.cuda(), tab.cuda(), sl.cuda(), prefix, ws=ws)
+        assert fa.device_status(ws=ws) == 0
+        assert_decode(got, decode_ref(q, k, v, table, lens))
