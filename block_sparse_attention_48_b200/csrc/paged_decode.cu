@@ -21,7 +21,7 @@
 // not depend on who comes last.
 //
 // Measured on a B200 (back to back, inputs not in L2): 8 sequences of 24k to 32k keys, Hkv 8
-// D 128, 137 us = 6.6 TB/s; 16 ragged ones up to 8191 keys 45 us; 24 with four drafted
+// D 128, 138 us = 6.55 TB/s; 16 ragged ones up to 8191 keys 45 us; 24 with four drafted
 // tokens, a window of 4096 and capped scores, Hkv 8 D 64, 40 us; one of 700 keys 8.3 us.
 // What the short ones are over their bytes is the start (the lengths, the table and the
 // first pages one after the other, 4 us), unequal shares of the memory's bandwidth (the

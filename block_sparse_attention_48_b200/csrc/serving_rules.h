@@ -51,8 +51,10 @@ inline int64_t pages_of_a_segment(int64_t pages_per_seq, int64_t window, int64_t
 // 26.7 / 22.0; 9 of 5000 (4 rows, D 64) 16.4 / 10.7.  Unequal lengths gain less or lose, their
 // shares running over two segments: 8 of 4000 to 8000 (16 rows, D 128) 34.7 / 30.1; 9 of 3746
 // to 4998 (4 rows, D 64) 14.6 / 15.1; 6 of 2000 to 5700 (16 rows, D 128) 22.0 / 24.6; 9 of 1200
-// to 2500 (16 rows, D 128) 15.5 / 21.6.  (By the page table's width: a rule on the lengths
-// themselves, on the device, cost every call 0.3 us; all teams for unequal lengths with a team
+// to 2500 (16 rows, D 128) 15.5 / 21.6.  The table's width stands for the lengths, which are on
+// the device, so tables wider than the sequences need lose the gain: the segment of 30000 keys
+// takes 21.7 us with its 235 pages of table, 29.2 with 940, 57.1 with 7520.  (A rule on the
+// lengths themselves, on the device, cost every call 0.3 us; all teams for unequal lengths with a team
 // for every page, 0.1 us, and lost as often as it won: 15.4 -> 17.4, 13.6 -> 11.6.)
 inline int32_t teams_that_pay(int64_t segments, int64_t pages, int64_t rows, int64_t D, int64_t most)
 {
