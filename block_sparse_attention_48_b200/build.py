@@ -57,7 +57,7 @@ def _torch() -> tuple:
     """(directory, version) of the installed torch, without importing it."""
     where = importlib.util.find_spec("torch").submodule_search_locations[0]
     with open(os.path.join(where, "version.py")) as f:
-        return where, re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read()).group(1)
+        return where, re.search(r"__version__[^=\n]*=\s*['\"]([^'\"]+)", f.read()).group(1)
 
 
 def build_binding(force: bool = False) -> str:

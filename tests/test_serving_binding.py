@@ -51,7 +51,7 @@ def test_another_torch_builds_the_binding_again(tmp_path, monkeypatch):
         open(cmd[cmd.index("-o") + 1], "w").close()
     monkeypatch.setattr(build.subprocess, "check_call", compile_)
     for version, builds in (("2.11.0+cu128", 1), ("2.11.0+cu128", 1), ("2.12.0", 2), ("2.12.0", 2), ("2.11.0+cu128", 3)):
-        (torch_dir / "version.py").write_text(f"from typing import Optional\n__version__ = '{version}'\ncuda = '12.8'\n")
+        (torch_dir / "version.py").write_text(f"from typing import Optional\n__version__{': str' if builds > 1 else ''} = '{version}'\n")
         build.build_binding()
         assert len(compiled) == builds, version
     os.utime(build.BINDING, (0, 0))  # older than its source
