@@ -22,12 +22,12 @@
 // O is rarely rescaled.
 //
 // Measured on a B200, 128 sequences behind 16384 shared keys, Hq 32 Hkv 8 D 128, own parts of
-// 128 to 777 keys: 82.6 us a call, 74 of them the kernel, 11 the join (under ncu).  A pair of tiles takes 3330 cycles, of which the
-// products need 2050 (whole tiles with one buffer: 4280): 1.4 PFLOP/s over the prefix alone
-// with all SMs.  Without the exponentials it would be 3200, without the products 2900, and
-// 1750 with nothing but the barriers; a quarter of the exponentials by polynomial changed
-// nothing.  One kernel after the other, each on all SMs, took 104 us (cold caches), side by
-// side 96, in one kernel with the split by cost 80.
+// 128 to 777 keys: 82.6 us a call, 74 of them the kernel and 11 the join (under ncu).  A pair
+// of tiles takes 3330 cycles, of which the products need 2050 (whole tiles with one buffer:
+// 4280): 1.4 PFLOP/s over the prefix alone with all SMs.  Without the exponentials it would be
+// 3200, without the products 2900, and 1750 with nothing but the barriers; a quarter of the
+// exponentials by polynomial changed nothing.  One kernel after the other, each on all SMs,
+// took 104 us (cold caches), side by side 96, in one kernel with the split by cost 80.
 #include <mutex>
 #include <vector>
 
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             v[3] = fmaf(y.w, f, v[3] * f0);
         };
         // Parts whose loads are issued together (which an unrolled loop alone does not bring
-        // about: 2 sequences of 8 rows behind 4096 shared pages 112 us, so 91).
+        // about: 5 sequences of 16 rows behind 300 shared pages 79.8 us, so 60.2; by four parts,
+        // which leave the kernel 60 registers instead of 85, 82.5).
         constexpr int U = 8;
         for (int k = 0; k < parts; k += U) {
             float2 w[U];
